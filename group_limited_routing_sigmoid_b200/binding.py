@@ -24,7 +24,8 @@ BEAM_ERR_TIMEOUT = -5
 BEAM_ERR_CHECK = -6
 BEAM_ERR_RANGE = -7
 
-# every entry point declared in include/beam_moe.h
+# every entry point declared in include/ (the beam_mx_*, beam_rms_norm,
+# beam_route_scores and beam_ops_* ones are wrapped in ops.py)
 SYMBOLS = (
     "beam_moe_create", "beam_moe_create_dense", "beam_moe_create_nvfp4", "beam_nvfp4_dequant",
     "beam_moe_route", "beam_moe_route_static", "beam_moe_router_logits", "beam_moe_route_logits",
@@ -37,6 +38,9 @@ SYMBOLS = (
     "beam_moe_profile_begin",
     "beam_moe_profile_end", "beam_moe_check_wait_timeout", "beam_moe_last_error",
     "beam_moe_create_error", "beam_moe_destroy",
+    "beam_mx_scale_bytes", "beam_mx_tensor_scale", "beam_mx_quantize", "beam_mx_dequantize",
+    "beam_mx_tile_scales", "beam_mx_matmul", "beam_rms_norm", "beam_route_scores",
+    "beam_ops_status", "beam_ops_error",
 )
 
 _lib = None
@@ -84,13 +88,24 @@ def library() -> ctypes.CDLL:
         lib.beam_moe_profile_begin.argtypes = [P, I]
         lib.beam_moe_profile_end.argtypes = [P, P, P]
         lib.beam_moe_last_error.argtypes = [P]
-        lib.beam_moe_last_error.restype = ctypes.c_char_p
         lib.beam_moe_create_error.argtypes = []
-        lib.beam_moe_create_error.restype = ctypes.c_char_p
         lib.beam_moe_destroy.argtypes = [P]
+        L = ctypes.c_longlong
+        lib.beam_mx_scale_bytes.argtypes = [I, L, I, I]
+        lib.beam_mx_tensor_scale.argtypes = [P, P, I, L, I, L, P]
+        lib.beam_mx_quantize.argtypes = [P, P, I, L, I, L, I, I, P, P, P]
+        lib.beam_mx_dequantize.argtypes = [P, P, P, P, I, I, L, I, P, I, L]
+        lib.beam_mx_tile_scales.argtypes = [P, I, P, L, I, P]
+        lib.beam_mx_matmul.argtypes = [P, I, P, P, P, I, P, P, P, I, I, I, P, I, L]
+        lib.beam_rms_norm.argtypes = [P, P, I, L, P, I, L, P, L, F, F, P, F, I, I, P, I, L, P, P, I]
+        lib.beam_route_scores.argtypes = [P, P, I, I, L, I, P, I, I, I, I, I, F, P, P]
+        lib.beam_ops_status.argtypes = [P]
+        lib.beam_ops_error.argtypes = []
         for name in SYMBOLS:
-            if name not in ("beam_moe_last_error", "beam_moe_create_error"):
-                getattr(lib, name).restype = I
+            getattr(lib, name).restype = I
+        for name in ("beam_moe_last_error", "beam_moe_create_error", "beam_ops_error"):
+            getattr(lib, name).restype = ctypes.c_char_p
+        lib.beam_mx_scale_bytes.restype = L
         _lib = lib
     return _lib
 

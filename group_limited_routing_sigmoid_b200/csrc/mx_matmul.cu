@@ -1,0 +1,529 @@
+// Product of two microscaled operands on the block-scaled tensor cores
+// (beam_mx_matmul):  out[t][n] = ga gw sum_k a[t][k] w[n][k].
+//
+// The MMA multiplies elements and block scales itself (tcgen05.mma
+// .block_scale): codes come from shared memory, scales from tensor memory,
+// sums stay in FP32 there.  The side with more rows (or the tokens, when both
+// sides have more than 128) is the MMA's A operand, in tiles of 128 rows; the
+// other is B, in tiles of BN = 16 .. 256 rows.
+//
+//   warp 0      one lane loads stages: a 128-byte wide box of codes of either
+//               side (128B swizzle) and the 512-byte scale tiles that go with
+//               it, by TMA and bulk copies into a ring
+//   warp 1      one lane copies a stage's scale tiles to tensor memory
+//               (tcgen05.cp, replicated to the four lane quadrants) and issues
+//               its four MMAs
+//   warps 2-9   epilogue: tensor memory to registers, tensor scales, rounding,
+//               stores
+//
+// Where there are fewer tiles than SMs, the K steps of a tile are split over
+// the CTAs of a cluster; each leaves its FP32 tile in its own shared memory
+// and sums a share of the columns over all of them, in rank order, so results
+// do not depend on timing and no workspace is needed.
+#include <atomic>
+
+#include "ops_common.cuh"
+
+namespace beam {
+namespace {
+
+using namespace ops;
+
+enum Kind { kNv = 0, kMx4 = 1, kMx8 = 2 };
+
+constexpr int kTileP = 128;
+constexpr int kRowBytes = 128;            // bytes of a row in a stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr long long kWaitLimitNs = 2000000000ll;
+
+// Sticky status word of the device (beam_ops_status).
+__device__ int g_ops_status;
+
+struct MatmulArgs {
+    const uint8_t *p_scales, *q_scales;
+    const float *ga, *gw;
+    void *out;
+    long long ldo;
+    int P, Q;              // rows of the A and B side
+    int p_tiles, q_tiles;
+    int nst;               // stages of K
+    int ksteps;            // MMA K steps in all
+    int n4;                // scale tiles along K
+    int split;             // CTAs that share a tile's K steps (the cluster)
+    int swap;              // 1: the A side holds the weights
+    int dtype;
+    uint32_t idesc;
+    uint32_t tx_codes;     // bytes a stage's two code boxes complete
+};
+
+template <int KIND, int BN>
+struct Cfg {
+    static constexpr int CPS = KIND == kNv ? 4 : KIND == kMx4 ? 2 : 1;   // scale tiles a stage and 128 rows
+    static constexpr int NQB = BN > 128 ? BN / 128 : 1;                  // 128-row scale blocks of B
+    static constexpr int P_BYTES = kTileP * kRowBytes;
+    static constexpr int Q_BYTES = BN * kRowBytes;
+    static constexpr int SF_BYTES = CPS * 512 * (1 + NQB);
+    static constexpr int STAGE = P_BYTES + Q_BYTES + (SF_BYTES + 1023) / 1024 * 1024;
+    static constexpr int SF_COLS = CPS * 4 * (1 + NQB);
+    // tiles of up to 64 columns: half an SM, so that two CTAs share one
+    static constexpr int BUDGET = BN <= 64 ? 110 * 1024 : 224 * 1024;
+    static constexpr int FIT = BUDGET / STAGE;
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int TMEM_COLS = BN <= 64 ? 256 : 512;
+    static constexpr int NBUF = 2 * BN + STAGES * SF_COLS <= TMEM_COLS ? 2 : 1;
+    static constexpr int SF0 = NBUF * BN;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+    static constexpr int CTAS_PER_SM = BN <= 64 ? 2 : 1;
+    static_assert(STAGES >= 3 && SF0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory");
+    static_assert(SMEM <= 232448 && BN * kTileP * 4 <= STAGES * STAGE, "shared memory");
+};
+
+// tcgen05.cp of one 512-byte scale tile: 32 rows of 16 bytes to lanes 0-31,
+// four columns, replicated to the other three lane quadrants.
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t smem)
+{
+    // no swizzle, 8 x 16-byte core matrices 128 bytes apart
+    const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)8u << 16) | ((uint64_t)8u << 32) |
+                       ((uint64_t)1u << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate)
+{
+    if constexpr (KIND == kNv)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else if constexpr (KIND == kMx4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: bits 4-5 scale id of B,
+// 7-9 / 10-12 element types of A / B (E2M1: 1 in the 4-bit kinds, 5 in
+// mxf8f6f4; E4M3: 0), 17-22 N >> 3, 23 scale type (1: UE8M0, 0: E4M3), 27-28
+// M >> 7, 29-30 scale id of A.
+uint32_t idesc_of(int kind, int n, bool a_fp4, bool b_fp4)
+{
+    const uint32_t fa = kind == kMx8 ? (a_fp4 ? 5u : 0u) : 1u, fb = kind == kMx8 ? (b_fp4 ? 5u : 0u) : 1u;
+    return (fa << 7) | (fb << 10) | ((uint32_t)(n >> 3) << 17) | (kind == kNv ? 0u : 1u << 23) | (1u << 27);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void put(void *out, int dtype, size_t at, float v)
+{
+    if (dtype == BEAM_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+    else if (dtype == BEAM_F16) static_cast<__half *>(out)[at] = __float2half_rn(v);
+    else static_cast<float *>(out)[at] = v;
+}
+
+template <int KIND, int BN>
+__global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
+    mx_matmul_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                     const MatmulArgs p)
+{
+    using C = Cfg<KIND, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(base_ptr + C::STAGES * C::STAGE);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *tfull = empty + C::STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtl ctl{&g_ops_status, kWaitLimitNs};
+    const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 32 * kEpiWarps);
+        }
+        mbar_init(smem_u32(drain), 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmP);
+        tma_prefetch_desc(&tmQ);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int total = status_is_set(ctl.status) ? 0 : p.p_tiles * p.q_tiles;
+    const int first = blockIdx.x / p.split, stride = gridDim.x / p.split;
+    const int ks0 = (int)((long long)p.nst * rank / p.split), ks1 = (int)((long long)p.nst * (rank + 1) / p.split);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ loads
+            const uint64_t pol_p = p.swap ? l2_policy_evict_first() : l2_policy_evict_normal();
+            const uint64_t pol_q = l2_policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int item = first; item < total && ok; item += stride) {
+                const int pt = item % p.p_tiles, qt = item / p.p_tiles;
+                const int nqb = min(C::NQB, (p.Q - qt * BN + 127) / 128);   // scale blocks that exist
+                const int qb = BN >= 128 ? qt * C::NQB : 0;                 // BN < 128: one tile of B
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    const int c0 = ks * C::CPS, nc = min(C::CPS, p.n4 - c0);
+                    mbar_arrive_expect_tx(fb, p.tx_codes + (uint32_t)(nc * 512 * (1 + nqb)));
+                    // x: bytes for the byte maps, elements for the 4-bit map (both 128 a stage)
+                    tma_load_2d(sp, &tmP, ks * kRowBytes, pt * kTileP, fb, pol_p);
+                    tma_load_2d(sq, &tmQ, ks * kRowBytes, qt * BN, fb, pol_q);
+                    bulk_load(sf, p.p_scales + ((size_t)pt * p.n4 + c0) * 512, nc * 512, fb);
+                    for (int b = 0; b < nqb; ++b)
+                        bulk_load(sf + C::CPS * 512 * (1 + b), p.q_scales + ((size_t)(qb + b) * p.n4 + c0) * 512,
+                                  nc * 512, fb);
+                    ++issued;
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                // copies in flight land before the CTA leaves
+                long long n = issued < C::STAGES ? issued : C::STAGES;
+                for (; n > 0; --n) {
+                    if (stage == 0) stage = C::STAGES - 1, phase ^= 1u;
+                    else --stage;
+                    mbar_wait_drain(smem_u32(&full[stage]), phase, ctl.limit_ns);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------ MMAs
+            int stage = 0, iter = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            for (int item = first; item < total && ok; item += stride, ++iter) {
+                const int acc = iter % C::NBUF;
+                const uint32_t d = tmem + acc * BN;
+                if (!mbar_wait(smem_u32(&tempty[acc]), ((uint32_t)(iter / C::NBUF) & 1u) ^ 1u, ctl)) break;
+                tc_fence_after();
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
+                    // a column set per ring stage: a copy never meets an
+                    // earlier stage's MMAs still reading
+                    const uint32_t tsf = tmem + C::SF0 + stage * C::SF_COLS;
+                    const uint32_t tsfq = tsf + C::CPS * 4;
+                    const int nc = min(C::CPS, p.n4 - ks * C::CPS);
+                    for (int c = 0; c < nc; ++c) {
+                        scale_copy(tsf + c * 4, sf + c * 512);
+#pragma unroll
+                        for (int b = 0; b < C::NQB; ++b)
+                            scale_copy(tsfq + (c * C::NQB + b) * 4, sf + (C::CPS * (1 + b) + c) * 512);
+                    }
+                    const int steps = min(4, p.ksteps - ks * 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j < steps) {
+                            const int c = KIND == kNv ? j : KIND == kMx4 ? j / 2 : 0;
+                            const uint32_t id = KIND == kNv ? 0u : KIND == kMx4 ? (uint32_t)(j & 1) * 2u : (uint32_t)j;
+                            mma_scaled<KIND>(d, umma_desc_sw128(sp + j * 32), umma_desc_sw128(sq + j * 32),
+                                             p.idesc | (id << 4) | (id << 29), tsf + c * 4, tsfq + c * C::NQB * 4,
+                                             (ks > ks0 || j > 0) ? 1u : 0u);
+                        }
+                    }
+                    any = true;
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+                }
+                if (ok) umma_commit(smem_u32(&tfull[acc]));
+            }
+            if (any) {   // every MMA is complete before tensor memory is released
+                umma_commit(smem_u32(drain));
+                mbar_wait_drain(smem_u32(drain), 0, ctl.limit_ns);
+            }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        constexpr int CH = BN >= 64 ? 32 : 16;
+        const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
+        int iter = 0;
+        for (int item = first; item < total; item += stride, ++iter) {
+            const int acc = iter % C::NBUF;
+            const bool ok = mbar_wait(smem_u32(&tfull[acc]), (uint32_t)(iter / C::NBUF) & 1u, ctl);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int pt = item % p.p_tiles, qt = item / p.p_tiles;
+            const int prow = pt * kTileP + quad * 32 + lane;
+            const uint32_t taddr = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+            for (int c0 = half * CH; c0 < BN; c0 += 2 * CH) {
+                uint32_t v[CH];
+                if constexpr (CH == 32) tmem_ld32(taddr + c0, v);
+                else tmem_ld16(taddr + c0, v);
+                tmem_ld_wait();
+                if (p.split > 1) {
+                    float *red = reinterpret_cast<float *>(base_ptr);   // [column][128 rows]
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) red[(c0 + j) * kTileP + quad * 32 + lane] = __uint_as_float(v[j]);
+                } else {
+                    const int q0 = qt * BN + c0;
+                    if (prow < p.P) {
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            if (q0 + j < p.Q) {
+                                const float y = __uint_as_float(v[j]) * ga * gw;
+                                put(p.out, p.dtype,
+                                    p.swap ? (size_t)(q0 + j) * p.ldo + prow : (size_t)prow * p.ldo + q0 + j, y);
+                            }
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&tempty[acc]));
+        }
+    }
+
+    if (p.split > 1) {
+        __syncwarp();
+        cluster_sync();   // every CTA's FP32 tile is in its shared memory
+        const int pt = first % p.p_tiles, qt = first / p.p_tiles;
+        if (warp >= 2 && first < total) {
+            const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
+            const int tid = threadIdx.x - 64;
+            const int cols = min(BN, p.Q - qt * BN);
+            const int lo = cols * rank / p.split, hi = cols * (rank + 1) / p.split;
+            const int row = tid & 127;
+            const int prow = pt * kTileP + row;
+            for (int c = lo + (tid >> 7); c < hi; c += 2) {
+                float y = 0.f;
+                for (int r = 0; r < p.split; ++r)
+                    y += ld_cluster_f32(mapa_shared(base + (uint32_t)(c * kTileP + row) * 4u, (uint32_t)r));
+                y = y * ga * gw;
+                const int q = qt * BN + c;
+                if (prow < p.P)
+                    put(p.out, p.dtype, p.swap ? (size_t)q * p.ldo + prow : (size_t)prow * p.ldo + q, y);
+            }
+        }
+        __syncwarp();
+        cluster_sync();   // no CTA leaves while another may read its tile
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static std::atomic<EncodeTiledFn> fn{nullptr};
+    EncodeTiledFn f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess) {
+            f = reinterpret_cast<EncodeTiledFn>(p);
+            fn.store(f, std::memory_order_release);
+        }
+    }
+    return f;
+}
+
+// Codes as a 2-D tensor of 128-byte wide boxes, 128B swizzle.  Bytes, except
+// 4-bit codes beside 8-bit ones: those are spread by the copy to the 16-byte
+// groups (8 bytes of codes, 8 of padding) that the mixed MMA reads.
+bool code_map(CUtensorMap *m, const uint8_t *codes, int format, bool spread, long long rows, int K, int box_rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t pitch = format == BEAM_MXFP8 ? K : K / 2;
+    cuuint64_t dims[2] = {spread ? (cuuint64_t)K : pitch, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {pitch};
+    cuuint32_t box[2] = {kRowBytes, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+               const_cast<uint8_t *>(codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND, int BN>
+cudaError_t launch(const CUtensorMap &tp, const CUtensorMap &tq, const MatmulArgs &a, int ctas, cudaStream_t s)
+{
+    using C = Cfg<KIND, BN>;
+    cudaError_t e = cudaFuncSetAttribute(mx_matmul_kernel<KIND, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)a.split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = a.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, mx_matmul_kernel<KIND, BN>, tp, tq, a);
+}
+
+template <int KIND>
+cudaError_t launch_bn(int bn, const CUtensorMap &tp, const CUtensorMap &tq, const MatmulArgs &a, int ctas,
+                      cudaStream_t s)
+{
+    switch (bn) {
+        case 16: return launch<KIND, 16>(tp, tq, a, ctas, s);
+        case 32: return launch<KIND, 32>(tp, tq, a, ctas, s);
+        case 64: return launch<KIND, 64>(tp, tq, a, ctas, s);
+        case 128: return launch<KIND, 128>(tp, tq, a, ctas, s);
+        default: return launch<KIND, 256>(tp, tq, a, ctas, s);
+    }
+}
+
+}  // namespace
+}  // namespace beam
+
+extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes, const uint8_t *a_scales,
+                              const float *a_tensor_scale, int w_format, const uint8_t *w_codes,
+                              const uint8_t *w_scales, const float *w_tensor_scale, int T, int N, int K,
+                              void *out, int dtype, long long ldo)
+{
+    using namespace beam;
+    using namespace beam::ops;
+    if (!format_ok(a_format) || !format_ok(w_format)) return fail(BEAM_ERR_INVALID_ARG, "format %d x %d", a_format, w_format);
+    if (!dtype_ok(dtype)) return fail(BEAM_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (T < 0 || N < 0 || T >= (1 << 27) || N >= (1 << 27) || K <= 0)
+        return fail(BEAM_ERR_INVALID_ARG, "T and N must be in 0 .. 2^27 - 1 and K positive");
+    int kind;
+    if (a_format == BEAM_NVFP4 && w_format == BEAM_NVFP4) kind = kNv;
+    else if (a_format == BEAM_MXFP4 && w_format == BEAM_MXFP4) kind = kMx4;
+    else if (a_format == BEAM_MXFP8 && (w_format == BEAM_MXFP4 || w_format == BEAM_MXFP8)) kind = kMx8;
+    else return fail(BEAM_ERR_UNSUPPORTED, "formats %d x %d have no product", a_format, w_format);
+    const int k_unit = kind == kMx8 ? 128 : 64;
+    if (K % k_unit != 0) return fail(BEAM_ERR_UNSUPPORTED, "K must be a multiple of %d, got %d", k_unit, K);
+    if (T == 0 || N == 0) return BEAM_OK;
+    if (!a_codes || !a_scales || !w_codes || !w_scales || !out)
+        return fail(BEAM_ERR_INVALID_ARG, "codes, scales and out are required");
+    if (ldo < N) return fail(BEAM_ERR_INVALID_ARG, "ldo is below N");
+    if (!aligned(a_codes, 32) || !aligned(a_scales, 32) || !aligned(w_codes, 32) || !aligned(w_scales, 32) ||
+        !aligned(out, dtype_size(dtype)) || !aligned(a_tensor_scale, 4) || !aligned(w_tensor_scale, 4))
+        return fail(BEAM_ERR_INVALID_ARG, "a pointer is not aligned");
+    const int sms = sm_count();
+    if (!sms) return fail(BEAM_ERR_CUDA, "no CUDA device");
+
+    // the A side (128-row tiles): the tokens when both sides have more than
+    // 128 rows (their stores are rows of out), else the longer side
+    const bool swap = T <= 128 || N <= 128 ? N >= T : false;
+    MatmulArgs a{};
+    a.swap = swap;
+    a.P = swap ? N : T;
+    a.Q = swap ? T : N;
+    a.p_scales = swap ? w_scales : a_scales;
+    a.q_scales = swap ? a_scales : w_scales;
+    a.ga = a_tensor_scale;
+    a.gw = w_tensor_scale;
+    a.out = out;
+    a.ldo = ldo;
+    a.dtype = dtype;
+    const int stage_k = kind == kMx8 ? 128 : 256, step_k = kind == kMx8 ? 32 : 64;
+    a.nst = (K + stage_k - 1) / stage_k;
+    a.ksteps = K / step_k;
+    a.n4 = (K / block_of(a_format) + 3) / 4;
+    int bn = 16;
+    while (bn < a.Q && bn < 256) bn *= 2;
+    a.p_tiles = (a.P + kTileP - 1) / kTileP;
+    // 256 columns only where there are tiles for every SM
+    if (bn == 256 && (long long)a.p_tiles * ((a.Q + 255) / 256) < sms) bn = 128;
+    a.q_tiles = (a.Q + bn - 1) / bn;
+    const long long tiles = (long long)a.p_tiles * a.q_tiles;
+    const int slots = sms * (bn <= 64 ? 2 : 1);
+    a.split = 1;
+    while (a.split < 8 && tiles * a.split * 2 <= slots && a.split * 2 <= a.nst) a.split *= 2;
+    const int ctas = a.split > 1 ? (int)tiles * a.split : (int)(tiles < slots ? tiles : slots);
+    const bool p_fp4 = (swap ? w_format : a_format) != BEAM_MXFP8, q_fp4 = (swap ? a_format : w_format) != BEAM_MXFP8;
+    a.idesc = idesc_of(kind, bn, p_fp4, q_fp4);
+    // a spread copy counts the bytes of its packed codes
+    a.tx_codes = (uint32_t)(kTileP * (kind == kMx8 && p_fp4 ? kRowBytes / 2 : kRowBytes) +
+                            bn * (kind == kMx8 && q_fp4 ? kRowBytes / 2 : kRowBytes));
+    CUtensorMap tp, tq;
+    if (!code_map(&tp, swap ? w_codes : a_codes, swap ? w_format : a_format, kind == kMx8 && p_fp4, a.P, K, kTileP) ||
+        !code_map(&tq, swap ? a_codes : w_codes, swap ? a_format : w_format, kind == kMx8 && q_fp4, a.Q, K, bn))
+        return fail(BEAM_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (kind == kNv) e = launch_bn<kNv>(bn, tp, tq, a, ctas, s);
+    else if (kind == kMx4) e = launch_bn<kMx4>(bn, tp, tq, a, ctas, s);
+    else e = launch_bn<kMx8>(bn, tp, tq, a, ctas, s);
+    return check_cuda(e, "beam_mx_matmul");
+}
+
+extern "C" int beam_ops_status(void *stream)
+{
+    using namespace beam;
+    using namespace beam::ops;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int host = 0;
+    const int zero = 0;
+    if (int rc = check_cuda(cudaMemcpyFromSymbolAsync(&host, g_ops_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s),
+                            "beam_ops_status")) return rc;
+    if (int rc = check_cuda(cudaStreamSynchronize(s), "beam_ops_status")) return rc;
+    if (host != 0) {
+        if (int rc = check_cuda(cudaMemcpyToSymbolAsync(g_ops_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s),
+                                "beam_ops_status")) return rc;
+        if (int rc = check_cuda(cudaStreamSynchronize(s), "beam_ops_status")) return rc;
+    }
+    return host;
+}
