@@ -22,109 +22,46 @@
 // do not depend on timing and no workspace is needed.
 #include <atomic>
 
-#include "ops_common.cuh"
+#include "mx_matmul.cuh"
 
 namespace beam {
 namespace {
 
-using namespace ops;
-
-enum Kind { kNv = 0, kMx4 = 1, kMx8 = 2 };
-
-constexpr int kTileP = 128;
-constexpr int kRowBytes = 128;            // bytes of a row in a stage
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr long long kWaitLimitNs = 2000000000ll;
+using namespace mx;
 
 // Sticky status word of the device (beam_ops_status).
 __device__ int g_ops_status;
 
-struct MatmulArgs {
-    const uint8_t *p_scales, *q_scales;
-    const float *ga, *gw;
-    void *out;
-    long long ldo;
-    int P, Q;              // rows of the A and B side
-    int p_tiles, q_tiles;
-    int nst;               // stages of K
-    int ksteps;            // MMA K steps in all
-    int n4;                // scale tiles along K
-    int split;             // CTAs that share a tile's K steps (the cluster)
-    int swap;              // 1: the A side holds the weights
-    int dtype;
-    uint32_t idesc;
-    uint32_t tx_codes;     // bytes a stage's two code boxes complete
-};
-
 template <int KIND, int BN>
 struct Cfg {
-    static constexpr int CPS = KIND == kNv ? 4 : KIND == kMx4 ? 2 : 1;   // scale tiles a stage and 128 rows
-    static constexpr int NQB = BN > 128 ? BN / 128 : 1;                  // 128-row scale blocks of B
+    static constexpr int NQB = 1;                                        // BN <= 128: one scale block of B
     static constexpr int P_BYTES = kTileP * kRowBytes;
     static constexpr int Q_BYTES = BN * kRowBytes;
-    static constexpr int SF_BYTES = CPS * 512 * (1 + NQB);
-    static constexpr int STAGE = P_BYTES + Q_BYTES + (SF_BYTES + 1023) / 1024 * 1024;
-    static constexpr int SF_COLS = CPS * 4 * (1 + NQB);
+    static constexpr int STAGE = P_BYTES + Q_BYTES + (scale_bytes(KIND, NQB) + 1023) / 1024 * 1024;
+    static constexpr int SF_COLS = scale_cols(KIND, NQB);
+    static constexpr int STAGING = BN == 128 ? kEpiWarps * 4096 : 0;
     // tiles of up to 64 columns: half an SM, so that two CTAs share one
-    static constexpr int BUDGET = BN <= 64 ? 110 * 1024 : 224 * 1024;
+    static constexpr int BUDGET = BN <= 64 ? 110 * 1024 : 224 * 1024 - STAGING;
     static constexpr int FIT = BUDGET / STAGE;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int TMEM_COLS = BN <= 64 ? 256 : 512;
-    static constexpr int NBUF = 2 * BN + STAGES * SF_COLS <= TMEM_COLS ? 2 : 1;
+    static constexpr int NBUF = 2;
     static constexpr int SF0 = NBUF * BN;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 256;
     static constexpr int CTAS_PER_SM = BN <= 64 ? 2 : 1;
     static_assert(STAGES >= 3 && SF0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory");
     static_assert(SMEM <= 232448 && BN * kTileP * 4 <= STAGES * STAGE, "shared memory");
 };
 
-// tcgen05.cp of one 512-byte scale tile: 32 rows of 16 bytes to lanes 0-31,
-// four columns, replicated to the other three lane quadrants.
-__device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t smem)
-{
-    // no swizzle, 8 x 16-byte core matrices 128 bytes apart
-    const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)8u << 16) | ((uint64_t)8u << 32) |
-                       ((uint64_t)1u << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
-
-template <int KIND>
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate)
-{
-    if constexpr (KIND == kNv)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-    else if constexpr (KIND == kMx4)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-
 // Instruction descriptor of the block-scaled kinds: bits 4-5 scale id of B,
 // 7-9 / 10-12 element types of A / B (E2M1: 1 in the 4-bit kinds, 5 in
 // mxf8f6f4; E4M3: 0), 17-22 N >> 3, 23 scale type (1: UE8M0, 0: E4M3), 27-28
 // M >> 7, 29-30 scale id of A.
-uint32_t idesc_of(int kind, int n, bool a_fp4, bool b_fp4)
+uint32_t idesc_of(int kind, int m, int n, bool a_fp4, bool b_fp4)
 {
     const uint32_t fa = kind == kMx8 ? (a_fp4 ? 5u : 0u) : 1u, fb = kind == kMx8 ? (b_fp4 ? 5u : 0u) : 1u;
-    return (fa << 7) | (fb << 10) | ((uint32_t)(n >> 3) << 17) | (kind == kNv ? 0u : 1u << 23) | (1u << 27);
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    return (fa << 7) | (fb << 10) | ((uint32_t)(n >> 3) << 17) | (kind == kNv ? 0u : 1u << 23) |
+           ((uint32_t)(m >> 7) << 27);
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
@@ -134,31 +71,25 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void put(void *out, int dtype, size_t at, float v)
-{
-    if (dtype == BEAM_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
-    else if (dtype == BEAM_F16) static_cast<__half *>(out)[at] = __float2half_rn(v);
-    else static_cast<float *>(out)[at] = v;
-}
-
 template <int KIND, int BN>
 __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
-    mx_matmul_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                     const MatmulArgs p)
+    mx_matmul_kernel(const __grid_constant__ Maps maps, const MatmulArgs p)
 {
     using C = Cfg<KIND, BN>;
+    constexpr int CPS = tiles_per_stage(KIND);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(base_ptr + C::STAGES * C::STAGE);
+    uint8_t *staging = base_ptr + C::STAGES * C::STAGE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + C::STAGING);
     uint64_t *empty = full + C::STAGES;
     uint64_t *tfull = empty + C::STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const WaitCtl ctl{&g_ops_status, kWaitLimitNs};
+    const WaitCtl ctl{p.status, kWaitLimitNs};
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
 
     if (warp == 0 && lane == 0) {
@@ -172,8 +103,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
         }
         mbar_init(smem_u32(drain), 1);
         fence_barrier_init();
-        tma_prefetch_desc(&tmP);
-        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&maps.p);
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.sp);
+        tma_prefetch_desc(&maps.sq);
     }
     if (warp == 1) {
         __syncwarp();
@@ -202,8 +135,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
             bool ok = true;
             for (int item = first; item < total && ok; item += stride) {
                 const int pt = item % p.p_tiles, qt = item / p.p_tiles;
-                const int nqb = min(C::NQB, (p.Q - qt * BN + 127) / 128);   // scale blocks that exist
-                const int qb = BN >= 128 ? qt * C::NQB : 0;                 // BN < 128: one tile of B
                 for (int ks = ks0; ks < ks1; ++ks) {
                     if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctl)) {
                         ok = false;
@@ -211,15 +142,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     }
                     const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
                     const uint32_t fb = smem_u32(&full[stage]);
-                    const int c0 = ks * C::CPS, nc = min(C::CPS, p.n4 - c0);
-                    mbar_arrive_expect_tx(fb, p.tx_codes + (uint32_t)(nc * 512 * (1 + nqb)));
+                    mbar_arrive_expect_tx(fb, p.tx);
                     // x: bytes for the byte maps, elements for the 4-bit map (both 128 a stage)
-                    tma_load_2d(sp, &tmP, ks * kRowBytes, pt * kTileP, fb, pol_p);
-                    tma_load_2d(sq, &tmQ, ks * kRowBytes, qt * BN, fb, pol_q);
-                    bulk_load(sf, p.p_scales + ((size_t)pt * p.n4 + c0) * 512, nc * 512, fb);
-                    for (int b = 0; b < nqb; ++b)
-                        bulk_load(sf + C::CPS * 512 * (1 + b), p.q_scales + ((size_t)(qb + b) * p.n4 + c0) * 512,
-                                  nc * 512, fb);
+                    tma_load_2d(sp, &maps.p, ks * kRowBytes, pt * kTileP, fb, pol_p);
+                    tma_load_2d(sq, &maps.q, ks * kRowBytes, qt * BN, fb, pol_q);
+                    tma_load_3d(sf, &maps.sp, ks * CPS, pt, fb);
+                    tma_load_3d(sf + CPS * 512, &maps.sq, ks * CPS, qt, fb);
                     ++issued;
                     if (++stage == C::STAGES) stage = 0, phase ^= 1u;
                 }
@@ -254,26 +182,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
                     // a column set per ring stage: a copy never meets an
                     // earlier stage's MMAs still reading
-                    const uint32_t tsf = tmem + C::SF0 + stage * C::SF_COLS;
-                    const uint32_t tsfq = tsf + C::CPS * 4;
-                    const int nc = min(C::CPS, p.n4 - ks * C::CPS);
-                    for (int c = 0; c < nc; ++c) {
-                        scale_copy(tsf + c * 4, sf + c * 512);
-#pragma unroll
-                        for (int b = 0; b < C::NQB; ++b)
-                            scale_copy(tsfq + (c * C::NQB + b) * 4, sf + (C::CPS * (1 + b) + c) * 512);
-                    }
-                    const int steps = min(4, p.ksteps - ks * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j < steps) {
-                            const int c = KIND == kNv ? j : KIND == kMx4 ? j / 2 : 0;
-                            const uint32_t id = KIND == kNv ? 0u : KIND == kMx4 ? (uint32_t)(j & 1) * 2u : (uint32_t)j;
-                            mma_scaled<KIND>(d, umma_desc_sw128(sp + j * 32), umma_desc_sw128(sq + j * 32),
-                                             p.idesc | (id << 4) | (id << 29), tsf + c * 4, tsfq + c * C::NQB * 4,
-                                             (ks > ks0 || j > 0) ? 1u : 0u);
-                        }
-                    }
+                    mma_stage<KIND, 1, C::NQB>(d, sp, sq, sf, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
+                                               min(4, p.ksteps - ks * 4), ks == ks0);
                     any = true;
                     umma_commit(smem_u32(&empty[stage]));
                     if (++stage == C::STAGES) stage = 0, phase ^= 1u;
@@ -288,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
     } else {
         // ---------------------------------------------------- epilogue
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        constexpr int CH = BN >= 64 ? 32 : 16;
+        constexpr int CH = BN >= 64 ? 32 : 16;          // columns read at a time
+        constexpr int SPAN = BN == 128 ? 64 : CH;       // columns a warp takes in turn
         const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
         int iter = 0;
         for (int item = first; item < total; item += stride, ++iter) {
@@ -297,28 +208,45 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const int pt = item % p.p_tiles, qt = item / p.p_tiles;
-            const int prow = pt * kTileP + quad * 32 + lane;
+            const int prow0 = pt * kTileP + quad * 32;
             const uint32_t taddr = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
-            for (int c0 = half * CH; c0 < BN; c0 += 2 * CH) {
-                uint32_t v[CH];
-                if constexpr (CH == 32) tmem_ld32(taddr + c0, v);
-                else tmem_ld16(taddr + c0, v);
-                tmem_ld_wait();
-                if (p.split > 1) {
-                    float *red = reinterpret_cast<float *>(base_ptr);   // [column][128 rows]
+            for (int c0 = half * SPAN; c0 < BN; c0 += 2 * SPAN) {
+#pragma unroll 1
+                for (int c1 = c0; c1 < c0 + SPAN; c1 += CH) {
+                    uint32_t r[CH];
+                    if constexpr (CH == 32) tmem_ld32(taddr + c1, r);
+                    else tmem_ld16(taddr + c1, r);
+                    tmem_ld_wait();
+                    if (p.split > 1) {
+                        float *red = reinterpret_cast<float *>(base_ptr);   // [column][128 rows]
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) red[(c0 + j) * kTileP + quad * 32 + lane] = __uint_as_float(v[j]);
-                } else {
-                    const int q0 = qt * BN + c0;
-                    if (prow < p.P) {
+                        for (int j = 0; j < CH; ++j) red[(c1 + j) * kTileP + quad * 32 + lane] = __uint_as_float(r[j]);
+                        continue;
+                    }
+                    float v[CH];
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) v[j] = __uint_as_float(r[j]) * ga * gw;
+                    const int q0 = qt * BN + c1;
+                    if constexpr (BN == 128) {
+                        if (!p.swap) {
+                            const int span = p.dtype == BEAM_F32 ? 32 : 64;
+                            const int line = (c1 - c0) % span;   // column of the staged line
+                            stage_columns(v, staging + (warp - 2) * 4096, lane, p.dtype, line / 32);
+                            if (line + 32 == span)
+                                flush_lines(staging + (warp - 2) * 4096, lane, p.dtype, p.out,
+                                            (size_t)prow0 * p.ldo + q0 - line, p.ldo, min(32, p.P - prow0),
+                                            min(span, p.Q - (q0 - line)), p.vec);
+                            continue;
+                        }
+                    }
+                    if (prow0 + lane < p.P) {
 #pragma unroll
                         for (int j = 0; j < CH; ++j)
-                            if (q0 + j < p.Q) {
-                                const float y = __uint_as_float(v[j]) * ga * gw;
+                            if (q0 + j < p.Q)
                                 put(p.out, p.dtype,
-                                    p.swap ? (size_t)(q0 + j) * p.ldo + prow : (size_t)prow * p.ldo + q0 + j, y);
-                            }
+                                    p.swap ? (size_t)(q0 + j) * p.ldo + prow0 + lane : (size_t)(prow0 + lane) * p.ldo + q0 + j,
+                                    v[j]);
                     }
                 }
             }
@@ -399,8 +327,23 @@ bool code_map(CUtensorMap *m, const uint8_t *codes, int format, bool spread, lon
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as a 3-D tensor {128 words, tiles along K, 128-row blocks}; the
+// box is a stage's tiles of `blocks` blocks.  Tiles past the end read as zero.
+bool scale_map(CUtensorMap *m, const uint8_t *scales, long long rows, int n4, int tiles, int blocks)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)n4, (cuuint64_t)((rows + 127) / 128)};
+    cuuint64_t strides[2] = {512, (cuuint64_t)n4 * 512};
+    cuuint32_t box[3] = {128, (cuuint32_t)tiles, (cuuint32_t)blocks};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int KIND, int BN>
-cudaError_t launch(const CUtensorMap &tp, const CUtensorMap &tq, const MatmulArgs &a, int ctas, cudaStream_t s)
+cudaError_t launch(const Maps &m, const MatmulArgs &a, int ctas, cudaStream_t s)
 {
     using C = Cfg<KIND, BN>;
     cudaError_t e = cudaFuncSetAttribute(mx_matmul_kernel<KIND, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -417,20 +360,35 @@ cudaError_t launch(const CUtensorMap &tp, const CUtensorMap &tq, const MatmulArg
     attr[1].val.clusterDim = {(unsigned)a.split, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mx_matmul_kernel<KIND, BN>, tp, tq, a);
+    return cudaLaunchKernelEx(&cfg, mx_matmul_kernel<KIND, BN>, m, a);
 }
 
 template <int KIND>
-cudaError_t launch_bn(int bn, const CUtensorMap &tp, const CUtensorMap &tq, const MatmulArgs &a, int ctas,
-                      cudaStream_t s)
+cudaError_t launch_bn(int bn, const Maps &m, const MatmulArgs &a, int ctas, cudaStream_t s)
 {
     switch (bn) {
-        case 16: return launch<KIND, 16>(tp, tq, a, ctas, s);
-        case 32: return launch<KIND, 32>(tp, tq, a, ctas, s);
-        case 64: return launch<KIND, 64>(tp, tq, a, ctas, s);
-        case 128: return launch<KIND, 128>(tp, tq, a, ctas, s);
-        default: return launch<KIND, 256>(tp, tq, a, ctas, s);
+        case 16: return launch<KIND, 16>(m, a, ctas, s);
+        case 32: return launch<KIND, 32>(m, a, ctas, s);
+        case 64: return launch<KIND, 64>(m, a, ctas, s);
+        default: return launch<KIND, 128>(m, a, ctas, s);
     }
+}
+
+// Device address of the status word, looked up once per device.
+std::atomic<int *> g_status_ptr[64];
+
+int *status_ptr()
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    int *p = g_status_ptr[dev].load(std::memory_order_acquire);
+    if (!p) {
+        void *v = nullptr;
+        if (cudaGetSymbolAddress(&v, g_ops_status) != cudaSuccess) return nullptr;
+        p = static_cast<int *>(v);
+        g_status_ptr[dev].store(p, std::memory_order_release);
+    }
+    return p;
 }
 
 }  // namespace
@@ -471,42 +429,54 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
     a.swap = swap;
     a.P = swap ? N : T;
     a.Q = swap ? T : N;
-    a.p_scales = swap ? w_scales : a_scales;
-    a.q_scales = swap ? a_scales : w_scales;
     a.ga = a_tensor_scale;
     a.gw = w_tensor_scale;
     a.out = out;
     a.ldo = ldo;
     a.dtype = dtype;
-    const int stage_k = kind == kMx8 ? 128 : 256, step_k = kind == kMx8 ? 32 : 64;
-    a.nst = (K + stage_k - 1) / stage_k;
-    a.ksteps = K / step_k;
-    a.n4 = (K / block_of(a_format) + 3) / 4;
+    a.vec = rows_aligned16(out, ldo, dtype);
+    a.status = status_ptr();
+    if (!a.status) return fail(BEAM_ERR_CUDA, "no device address of the status word");
+    a.nst = (K + stage_k(kind) - 1) / stage_k(kind);
+    a.ksteps = K / step_k(kind);
+    const int n4 = (K / block_of(a_format) + 3) / 4;
     int bn = 16;
-    while (bn < a.Q && bn < 256) bn *= 2;
+    while (bn < a.Q && bn < 128) bn *= 2;
     a.p_tiles = (a.P + kTileP - 1) / kTileP;
-    // 256 columns only where there are tiles for every SM
-    if (bn == 256 && (long long)a.p_tiles * ((a.Q + 255) / 256) < sms) bn = 128;
     a.q_tiles = (a.Q + bn - 1) / bn;
     const long long tiles = (long long)a.p_tiles * a.q_tiles;
-    const int slots = sms * (bn <= 64 ? 2 : 1);
+    // pairs of CTAs (256 x 256 tiles) where they fill the SMs
+    const int pair_p = (a.P + 255) / 256, pair_q = (a.Q + 255) / 256;
+    const bool pair = !swap && (long long)pair_p * pair_q * 2 >= sms;
     a.split = 1;
-    while (a.split < 8 && tiles * a.split * 2 <= slots && a.split * 2 <= a.nst) a.split *= 2;
-    const int ctas = a.split > 1 ? (int)tiles * a.split : (int)(tiles < slots ? tiles : slots);
+    const int slots = sms * (bn <= 64 ? 2 : 1);
+    if (pair) {
+        a.p_tiles = pair_p;
+        a.q_tiles = pair_q;
+        bn = 256;
+    } else {
+        while (a.split < 8 && tiles * a.split * 2 <= slots && a.split * 2 <= a.nst) a.split *= 2;
+    }
     const bool p_fp4 = (swap ? w_format : a_format) != BEAM_MXFP8, q_fp4 = (swap ? a_format : w_format) != BEAM_MXFP8;
-    a.idesc = idesc_of(kind, bn, p_fp4, q_fp4);
+    const bool p_spread = kind == kMx8 && p_fp4, q_spread = kind == kMx8 && q_fp4;
+    a.idesc = idesc_of(kind, pair ? 256 : 128, bn, p_fp4, q_fp4);
+    const int q_box = pair ? 128 : bn, cps = tiles_per_stage(kind), q_blocks = pair ? 2 : 1;
     // a spread copy counts the bytes of its packed codes
-    a.tx_codes = (uint32_t)(kTileP * (kind == kMx8 && p_fp4 ? kRowBytes / 2 : kRowBytes) +
-                            bn * (kind == kMx8 && q_fp4 ? kRowBytes / 2 : kRowBytes));
-    CUtensorMap tp, tq;
-    if (!code_map(&tp, swap ? w_codes : a_codes, swap ? w_format : a_format, kind == kMx8 && p_fp4, a.P, K, kTileP) ||
-        !code_map(&tq, swap ? a_codes : w_codes, swap ? a_format : w_format, kind == kMx8 && q_fp4, a.Q, K, bn))
+    a.tx = (uint32_t)(kTileP * (p_spread ? kRowBytes / 2 : kRowBytes) + q_box * (q_spread ? kRowBytes / 2 : kRowBytes) +
+                      cps * 512 * (1 + q_blocks));
+    Maps m;
+    if (!code_map(&m.p, swap ? w_codes : a_codes, swap ? w_format : a_format, p_spread, a.P, K, kTileP) ||
+        !code_map(&m.q, swap ? a_codes : w_codes, swap ? a_format : w_format, q_spread, a.Q, K, q_box) ||
+        !scale_map(&m.sp, swap ? w_scales : a_scales, a.P, n4, cps, 1) ||
+        !scale_map(&m.sq, swap ? a_scales : w_scales, a.Q, n4, cps, q_blocks))
         return fail(BEAM_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (kind == kNv) e = launch_bn<kNv>(bn, tp, tq, a, ctas, s);
-    else if (kind == kMx4) e = launch_bn<kMx4>(bn, tp, tq, a, ctas, s);
-    else e = launch_bn<kMx8>(bn, tp, tq, a, ctas, s);
+    const int ctas = a.split > 1 ? (int)tiles * a.split : (int)(tiles < slots ? tiles : slots);
+    if (pair) e = launch_pair(kind, m, a, sms, s);
+    else if (kind == kNv) e = launch_bn<kNv>(bn, m, a, ctas, s);
+    else if (kind == kMx4) e = launch_bn<kMx4>(bn, m, a, ctas, s);
+    else e = launch_bn<kMx8>(bn, m, a, ctas, s);
     return check_cuda(e, "beam_mx_matmul");
 }
 

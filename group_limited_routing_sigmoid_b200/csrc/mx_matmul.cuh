@@ -1,0 +1,199 @@
+// Shared pieces of the microscaled product's kernels (mx_matmul.cu: one CTA a
+// tile; mx_matmul_pair.cu: a CTA pair a tile).
+#pragma once
+
+#include "ops_common.cuh"
+
+namespace beam {
+namespace mx {
+
+using namespace ops;
+
+// Kinds of block-scaled MMA: NVFP4 (a scale per 16), MXFP4 (per 32) and
+// MXFP8 x MXFP8 / MXFP4 (per 32, 8-bit operands in shared memory).
+enum Kind { kNv = 0, kMx4 = 1, kMx8 = 2 };
+
+constexpr int kTileP = 128;               // rows of the A side per CTA
+constexpr int kRowBytes = 128;            // bytes of a row in a stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr long long kWaitLimitNs = 2000000000ll;
+
+// 512-byte scale tiles (128 rows x 4 scales) per stage and 128 rows.
+constexpr int tiles_per_stage(int kind) { return kind == kNv ? 4 : kind == kMx4 ? 2 : 1; }
+// K elements of a stage and of one MMA.
+constexpr int stage_k(int kind) { return kind == kMx8 ? 128 : 256; }
+constexpr int step_k(int kind) { return kind == kMx8 ? 32 : 64; }
+
+struct Maps {
+    CUtensorMap p, q;      // codes of the A and B side: boxes of 128 bytes x rows
+    CUtensorMap sp, sq;    // their scale tiles: [128-row blocks][tiles along K][512 bytes]
+};
+
+struct MatmulArgs {
+    const float *ga, *gw;
+    void *out;
+    long long ldo;
+    int *status;
+    int P, Q;              // rows of the A and B side
+    int p_tiles, q_tiles;
+    int nst;               // stages of K
+    int ksteps;            // MMA K steps in all
+    int split;             // CTAs that share a tile's K steps (the cluster)
+    int swap;              // 1: the A side holds the weights
+    int dtype;
+    int vec;               // 1: rows of out start on 16-byte boundaries
+    uint32_t idesc;
+    uint32_t tx;           // bytes one CTA's copies of a stage complete
+};
+
+cudaError_t launch_pair(int kind, const Maps &m, const MatmulArgs &a, int sms, cudaStream_t s);
+
+// Byte offset of a stage's scale tiles and the tensor-memory columns they
+// take, for `nqb` 128-row blocks of the B side.
+constexpr int scale_bytes(int kind, int nqb) { return tiles_per_stage(kind) * 512 * (1 + nqb); }
+constexpr int scale_cols(int kind, int nqb) { return tiles_per_stage(kind) * 4 * (1 + nqb); }
+
+// 3-D tile load of scale tiles: box {512 bytes, tiles of a stage, blocks}.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t y, int32_t z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// The same for a CTA pair: the barrier (a shared::cluster address) may be the other CTA's.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int32_t y, int32_t z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// tcgen05.cp of one 512-byte scale tile: 32 rows of 16 bytes to lanes 0-31,
+// four columns, replicated to the other three lane quadrants; for a pair, in
+// either CTA from its own shared memory.
+template <int CTAS>
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t smem)
+{
+    // no swizzle, 8 x 16-byte core matrices 128 bytes apart
+    const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)8u << 16) | ((uint64_t)8u << 32) |
+                       ((uint64_t)1u << 46);
+    if constexpr (CTAS == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+#define BEAM_MMA_SCALED(group, kind)                                                                        \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                          \
+                 "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),  \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                             \
+                 : "memory")
+
+template <int KIND, int CTAS>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate)
+{
+    if constexpr (CTAS == 1) {
+        if constexpr (KIND == kNv) BEAM_MMA_SCALED("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+        else if constexpr (KIND == kMx4) BEAM_MMA_SCALED("1", "kind::mxf4.block_scale.scale_vec::2X");
+        else BEAM_MMA_SCALED("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    } else {
+        if constexpr (KIND == kNv) BEAM_MMA_SCALED("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+        else if constexpr (KIND == kMx4) BEAM_MMA_SCALED("2", "kind::mxf4.block_scale.scale_vec::2X");
+        else BEAM_MMA_SCALED("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    }
+}
+#undef BEAM_MMA_SCALED
+
+// One stage: its scale tiles to tensor memory, then its MMAs.  sp, sq, sf:
+// the stage's codes and scales in shared memory; tsf: its columns.
+template <int KIND, int CTAS, int NQB>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, uint32_t sf, uint32_t tsf, uint32_t idesc,
+                                          int steps, bool first)
+{
+    constexpr int CPS = tiles_per_stage(KIND);
+    const uint32_t tsfq = tsf + CPS * 4;
+#pragma unroll
+    for (int c = 0; c < CPS; ++c) {
+        scale_copy<CTAS>(tsf + c * 4, sf + c * 512);
+#pragma unroll
+        for (int b = 0; b < NQB; ++b) scale_copy<CTAS>(tsfq + (c * NQB + b) * 4, sf + (CPS * (1 + b) + c) * 512);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j < steps) {
+            const int c = KIND == kNv ? j : KIND == kMx4 ? j / 2 : 0;
+            const uint32_t id = KIND == kNv ? 0u : KIND == kMx4 ? (uint32_t)(j & 1) * 2u : (uint32_t)j;
+            mma_scaled<KIND, CTAS>(d, umma_desc_sw128(sp + j * 32), umma_desc_sw128(sq + j * 32),
+                                   idesc | (id << 4) | (id << 29), tsf + c * 4, tsfq + c * NQB * 4,
+                                   (!first || j > 0) ? 1u : 0u);
+        }
+    }
+}
+
+__device__ __forceinline__ void put(void *out, int dtype, size_t at, float v)
+{
+    if (dtype == BEAM_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+    else if (dtype == BEAM_F16) static_cast<__half *>(out)[at] = __float2half_rn(v);
+    else static_cast<float *>(out)[at] = v;
+}
+
+// A warp's 32 rows x 32 columns of results (lane: row; v: its columns, scaled)
+// to rows row0 .. of out at column col, through the warp's 4 KB block of
+// shared memory so that a row's columns leave together: 16-byte units of a row
+// at their index xor the row's low bits, no bank met twice.
+//   elements of 2 bytes fill half a 128-byte line a row: `half_line` 0 or 1,
+//   and `flush` writes both halves (64 columns) out; 4 bytes: one line.
+__device__ __forceinline__ void stage_columns(const float (&v)[32], uint8_t *stg, int lane, int dtype, int half_line)
+{
+    uint4 *line = reinterpret_cast<uint4 *>(stg + lane * 128);
+    if (dtype == BEAM_F32) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            line[u ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                                              __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float *f = v + 8 * u;
+            line[(half_line * 4 + u) ^ (lane & 7)] =
+                dtype == BEAM_BF16
+                    ? make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]))
+                    : make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+        }
+    }
+}
+
+// Write the staged lines out: `rows` rows of `cols` columns (at most a line)
+// from out[at], rows ldo apart.  vec: 16-byte stores of whole units.
+__device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dtype, void *out, size_t at, long long ldo,
+                                            int rows, int cols, bool vec)
+{
+    const int es = dtype == BEAM_F32 ? 4 : 2, per = 16 / es;
+    __syncwarp();
+    uint8_t *o = static_cast<uint8_t *>(out) + at * es;
+    const size_t pitch = (size_t)ldo * es;
+    if (vec && cols % per == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3), u = lane & 7;
+            if (row < rows && u * per < cols)
+                *reinterpret_cast<uint4 *>(o + row * pitch + u * 16) =
+                    *reinterpret_cast<const uint4 *>(stg + row * 128 + ((u ^ (row & 7)) * 16));
+        }
+    } else {
+        for (int row = 0; row < rows; ++row)
+            for (int c = lane; c < cols; c += 32) {
+                const uint8_t *s = stg + row * 128 + (((c / per) ^ (row & 7)) * 16) + c % per * es;
+                if (es == 4) *reinterpret_cast<uint32_t *>(o + row * pitch + c * 4) = *reinterpret_cast<const uint32_t *>(s);
+                else *reinterpret_cast<uint16_t *>(o + row * pitch + c * 2) = *reinterpret_cast<const uint16_t *>(s);
+            }
+    }
+    __syncwarp();
+}
+
+}  // namespace mx
+}  // namespace beam

@@ -16,12 +16,11 @@ there.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from .binding import BEAM_OK, BeamMoEError, library
+from .binding import BEAM_ERR_INVALID_ARG, BEAM_OK, BeamMoEError, library
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
@@ -53,10 +52,10 @@ class NormResult(NamedTuple):
 
 
 def _key(table, value, name):
-    try:
-        return table[value]
-    except KeyError:
-        raise ValueError(f"{name}: expected one of {list(table)}, got {value!r}") from None
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name}: expected one of {list(table)}, got {value!r}")
+    return code
 
 
 def _check(rc: int):
@@ -64,141 +63,171 @@ def _check(rc: int):
         raise BeamMoEError(rc, library().beam_ops_error().decode())
 
 
-def _cuda(t, name: str, dtype=None, device=None):
-    """`t` is a CUDA tensor (of `dtype`, on `device`)."""
+# The checks below run on every call, beside kernels of a few microseconds:
+# they read each property of a tensor once and take the common case first.
+
+def _bad_device(t, name: str, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor, got {t.device if isinstance(t, torch.Tensor) else type(t)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the others on {device}")
-    return t
+    raise ValueError(f"{name}: on {t.device}, the others on {device}")
 
 
 def _rows(t, name: str, device=None):
-    """A 2-D matrix of a supported type whose rows are contiguous -> row stride."""
-    _cuda(t, name, device=device)
-    if t.dtype not in DTYPES:
+    """A matrix of a supported type on `device` (any CUDA device when None)
+    whose rows are contiguous -> (rows, columns, row stride, type code)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
+        _bad_device(t, name, device)
+    code = DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected one of {list(DTYPES)}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise TypeError(f"{name}: expected a matrix with contiguous rows, got shape {tuple(t.shape)}, "
-                        f"strides {t.stride()}")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise TypeError(f"{name}: rows overlap (stride {t.stride(0)} for {t.shape[1]} elements)")
-    return t.stride(0)
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        if t.is_contiguous():
+            return rows, cols, cols, code
+        if cols <= 1 or t.stride(1) == 1:
+            ld = t.stride(0)
+            if rows <= 1:
+                return rows, cols, cols, code
+            if ld >= cols:
+                return rows, cols, ld, code
+            raise TypeError(f"{name}: rows overlap (stride {ld} for {cols} elements)")
+    raise TypeError(f"{name}: expected a matrix with contiguous rows, got shape {tuple(shape)}, strides {t.stride()}")
 
 
 def _flat(t, name: str, dtype, n: int, device):
-    """A contiguous tensor of n elements."""
-    _cuda(t, name, dtype, device)
-    if not t.is_contiguous() or t.numel() != n:
+    """A contiguous tensor of n elements of `dtype` on `device` -> its address."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        _bad_device(t, name, device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
         raise TypeError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)} "
                         f"(contiguous={t.is_contiguous()})")
-    return t
+    return t.data_ptr()
 
 
-def _out(t, name: str, shape, dtype, device):
-    """An output matrix the caller gave -> row stride."""
-    ld = _rows(t, name, device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _out(t, name: str, rows: int, cols: int, dtype, device) -> int:
+    """An output matrix the caller gave -> its row stride."""
+    r, c, ld, _ = _rows(t, name, device)
+    if r != rows or c != cols or t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype} {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
     return ld
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
+# The current stream's handle without a Stream object around it, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _On:
-    """The device and stream a call runs on: `stream` or the device's current
-    stream; tensors are made there and, on another stream than the current
-    one, marked as used there."""
-
-    __slots__ = ("handle", "device", "contexts", "stream")
-
-    def __init__(self, device, stream):
-        self.device, self.contexts, self.stream = device, (), None
-        if device.index != torch.cuda.current_device():
-            self.contexts = (torch.cuda.device(device),)
-        current = torch.cuda.current_stream(device)
+def _on(device, stream, body, *args):
+    """body(stream handle, *args) on `device` and `stream` (None: the device's
+    current stream).  body returns (result, tensors it uses): those are made
+    on that stream and, where it is another one than the current stream,
+    marked as used there."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(_raw_stream(device.index), *args)[0]
+    with torch.cuda.device(device):
+        current = _raw_stream(device.index)
         if stream is None:
-            self.handle = current.cuda_stream
-            return
-        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if self.handle != current.cuda_stream:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(self.handle, device=device)
-            if stream.device != device:
-                raise ValueError(f"stream on {stream.device}, tensors on {device}")
-            self.stream = stream
-            self.contexts += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-
-    def used(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+            return body(current, *args)[0]
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle == current:
+            return body(current, *args)[0]
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle, device=device)
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        with torch.cuda.stream(stream):
+            result, tensors = body(handle, *args)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return result
 
 
 def ops_status(device=None, stream=None) -> int:
     """Wait for `stream`, then read and clear the device's status word."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _On(device, stream) as on:
-        return library().beam_ops_status(on.handle)
+    return _on(device, stream, lambda handle: (library().beam_ops_status(handle), ()))
 
 
 # --- microscaled operands ------------------------------------------------------
 
 def scale_bytes(format: str, rows: int, K: int, layout: str) -> int:
-    n = library().beam_mx_scale_bytes(_key(FORMATS, format, "format"), rows, K, _key(LAYOUTS, layout, "layout"))
-    if n < 0:
-        raise BeamMoEError(int(n), library().beam_ops_error().decode())
-    return n
+    """Bytes of the scales of a [rows, K] operand (beam_mx_scale_bytes)."""
+    block = BLOCK.get(format)
+    if block is None or layout not in LAYOUTS:
+        raise ValueError(f"format {format!r}, layout {layout!r}: expected one of {list(FORMATS)}, {list(LAYOUTS)}")
+    if rows < 0 or K <= 0 or K % block:
+        raise BeamMoEError(BEAM_ERR_INVALID_ARG,
+                           f"{format}: K must be a positive multiple of {block} and rows >= 0, got {rows} x {K}")
+    n = K // block
+    return rows * n if layout == "rows" else (rows + 127) // 128 * ((n + 3) // 4) * 512
 
 
 def _new_mx(format: str, layout: str, rows: int, K: int, device) -> MxTensor:
     n = scale_bytes(format, rows, K, layout)
-    codes = torch.empty(rows, K if format == "mxfp8" else K // 2, dtype=torch.uint8, device=device)
+    codes = torch.empty((rows, K if format == "mxfp8" else K // 2), dtype=torch.uint8, device=device)
     scales = torch.empty((rows, K // BLOCK[format]) if layout == "rows" else n, dtype=torch.uint8, device=device)
     return MxTensor(codes, scales, format, layout, rows, K)
 
 
 def _mx(q: MxTensor, name: str, device=None):
-    """Types, sizes and device of an operand's tensors."""
+    """Types, sizes and device of an operand's tensors -> (device, addresses of codes, scales, tensor scale)."""
     if not isinstance(q, MxTensor):
         raise TypeError(f"{name}: expected an MxTensor, got {type(q)}")
-    _key(FORMATS, q.format, name + ".format")
-    device = _cuda(q.codes, name + ".codes").device if device is None else device
-    _flat(q.codes, name + ".codes", torch.uint8, q.rows * (q.K if q.format == "mxfp8" else q.K // 2), device)
-    _flat(q.scales, name + ".scales", torch.uint8, scale_bytes(q.format, q.rows, q.K, q.layout), device)
-    if q.tensor_scale is not None:
-        _flat(q.tensor_scale, name + ".tensor_scale", torch.float32, 1, device)
-    return device
+    codes, scales, fmt, layout, rows, K, ts = q
+    n = scale_bytes(fmt, rows, K, layout)
+    if device is None:
+        if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+            _bad_device(codes, name + ".codes", device)
+        device = codes.device
+    return (device, _flat(codes, name, torch.uint8, rows * (K if fmt == "mxfp8" else K // 2), device),
+            _flat(scales, name, torch.uint8, n, device),
+            None if ts is None else _flat(ts, name, torch.float32, 1, device))
+
+
+def _given_mx(q: MxTensor, name: str, format: str, layout: str, rows: int, K: int, device):
+    """An operand to write into: of this format, layout and shape -> addresses of codes, scales."""
+    _, codes, scales, _ = _mx(q, name, device)
+    if (q.format, q.layout, q.rows, q.K) != (format, layout, rows, K):
+        raise ValueError(f"{name}: {q.format} {q.layout} {q.rows} x {q.K}, not {format} {layout} {rows} x {K}")
+    return codes, scales
+
+
+def _tensor_scale(handle, x, shape, out):
+    if out is None:
+        out = torch.empty(1, dtype=torch.float32, device=x.device)
+    rows, K, ld, code = shape
+    _check(library().beam_mx_tensor_scale(handle, x.data_ptr(), code, rows, K, ld,
+                                          _flat(out, "out", torch.float32, 1, x.device)))
+    return out, (x, out)
 
 
 def mx_tensor_scale(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The NVFP4 scale of x [rows, K]: the least power of two g with amax <= 6 * 448 * g (fp32 [1])."""
-    ld = _rows(x, "x")
-    if x.shape[1] < 1:
-        raise ValueError("x: rows of no elements")
-    with _On(x.device, stream) as on:
-        if out is None:
-            out = torch.empty(1, dtype=torch.float32, device=x.device)
-        _flat(out, "out", torch.float32, 1, x.device)
-        _check(library().beam_mx_tensor_scale(on.handle, _p(x), DTYPES[x.dtype], x.shape[0], x.shape[1], ld, _p(out)))
-        on.used(x, out)
-    return out
+    return _on(x.device, stream, _tensor_scale, x, _rows(x, "x"), out)
+
+
+def _quantize(handle, x, shape, format, f, layout, lay, tensor_scale, out):
+    rows, K, ld, code = shape
+    device = x.device
+    if out is None:
+        out = _new_mx(format, layout, rows, K, device)
+        codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        codes, scales = _given_mx(out, "out", format, layout, rows, K, device)
+    ts = None
+    if f == 0:
+        if tensor_scale is None:
+            tensor_scale, _ = _tensor_scale(handle, x, shape, None)
+        ts = _flat(tensor_scale, "tensor_scale", torch.float32, 1, device)
+    elif tensor_scale is not None:
+        raise ValueError(f"{format} has no tensor scale")
+    _check(library().beam_mx_quantize(handle, x.data_ptr(), code, rows, K, ld, f, lay, ts, codes, scales))
+    out = MxTensor(out.codes, out.scales, format, layout, rows, K, tensor_scale)
+    return out, (x, tensor_scale, out.codes, out.scales)
 
 
 def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale: Optional[torch.Tensor] = None,
@@ -209,77 +238,110 @@ def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale
     one more pass over x).  layout "rows" is what BeamMoE.nvfp4 and checkpoints
     take, "tiled" what mx_matmul takes.  `out`: an operand of the same shape to
     write into (its tensor_scale is not)."""
-    ld = _rows(x, "x")
-    rows, K = x.shape
-    f, l = _key(FORMATS, format, "format"), _key(LAYOUTS, layout, "layout")
-    with _On(x.device, stream) as on:
-        if out is None:
-            out = _new_mx(format, layout, rows, K, x.device)
-        else:
-            _mx(out, "out", x.device)
-            if (out.format, out.layout, out.rows, out.K) != (format, layout, rows, K):
-                raise ValueError(f"out: {out.format} {out.layout} {out.rows} x {out.K}, "
-                                 f"not {format} {layout} {rows} x {K}")
-        if format == "nvfp4":
-            if tensor_scale is None:
-                tensor_scale = mx_tensor_scale(x)
-            _flat(tensor_scale, "tensor_scale", torch.float32, 1, x.device)
-        elif tensor_scale is not None:
-            raise ValueError(f"{format} has no tensor scale")
-        _check(library().beam_mx_quantize(on.handle, _p(x), DTYPES[x.dtype], rows, K, ld, f, l, _p(tensor_scale),
-                                          _p(out.codes), _p(out.scales)))
-        on.used(x, tensor_scale, out.codes, out.scales)
-    return out._replace(tensor_scale=tensor_scale)
+    return _on(x.device, stream, _quantize, x, _rows(x, "x"), format, _key(FORMATS, format, "format"), layout,
+               _key(LAYOUTS, layout, "layout"), tensor_scale, out)
+
+
+def _dequantize(handle, q, device, codes, scales, ts, dtype, d, out):
+    if out is None:
+        out = torch.empty((q.rows, q.K), dtype=dtype, device=device)
+        ld = q.K
+    else:
+        ld = _out(out, "out", q.rows, q.K, dtype, device)
+    _check(library().beam_mx_dequantize(handle, codes, scales, ts, FORMATS[q.format], LAYOUTS[q.layout], q.rows, q.K,
+                                        out.data_ptr(), d, ld))
+    return out, (q.codes, q.scales, q.tensor_scale, out)
 
 
 def mx_dequantize(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of a microscaled operand, [rows, K]."""
-    device = _mx(q, "q")
-    d = _key(DTYPES, dtype, "dtype")
-    with _On(device, stream) as on:
-        if out is None:
-            out = torch.empty(q.rows, q.K, dtype=dtype, device=device)
-        ld = _out(out, "out", (q.rows, q.K), dtype, device)
-        _check(library().beam_mx_dequantize(on.handle, _p(q.codes), _p(q.scales), _p(q.tensor_scale),
-                                            FORMATS[q.format], LAYOUTS[q.layout], q.rows, q.K, _p(out), d, ld))
-        on.used(q.codes, q.scales, q.tensor_scale, out)
-    return out
+    device, codes, scales, ts = _mx(q, "q")
+    return _on(device, stream, _dequantize, q, device, codes, scales, ts, dtype, _key(DTYPES, dtype, "dtype"), out)
+
+
+def _tile(handle, q, device, scales):
+    tiled = torch.empty(scale_bytes(q.format, q.rows, q.K, "tiled"), dtype=torch.uint8, device=device)
+    _check(library().beam_mx_tile_scales(handle, FORMATS[q.format], scales, q.rows, q.K, tiled.data_ptr()))
+    return q._replace(scales=tiled, layout="tiled"), (q.scales, tiled)
 
 
 def mx_tile_scales(q: MxTensor, stream=None) -> MxTensor:
     """The same operand with its scales in the "tiled" layout (once, for a checkpoint's weights)."""
-    device = _mx(q, "q")
-    if q.layout == "tiled":
-        return q
-    with _On(device, stream) as on:
-        tiled = torch.empty(scale_bytes(q.format, q.rows, q.K, "tiled"), dtype=torch.uint8, device=device)
-        _check(library().beam_mx_tile_scales(on.handle, FORMATS[q.format], _p(q.scales), q.rows, q.K, _p(tiled)))
-        on.used(q.scales, tiled)
-    return q._replace(scales=tiled, layout="tiled")
+    device, _, scales, _ = _mx(q, "q")
+    return q if q.layout == "tiled" else _on(device, stream, _tile, q, device, scales)
+
+
+def _matmul(handle, a, w, device, pa, pw, dtype, d, out):
+    T, N = a.rows, w.rows
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=device)
+        ld = N
+    else:
+        ld = _out(out, "out", T, N, dtype, device)
+    _check(library().beam_mx_matmul(handle, FORMATS[a.format], pa[1], pa[2], pa[3], FORMATS[w.format], pw[1], pw[2],
+                                    pw[3], T, N, a.K, out.data_ptr(), d, ld))
+    return out, (a.codes, a.scales, a.tensor_scale, w.codes, w.scales, w.tensor_scale, out)
 
 
 def mx_matmul(a: MxTensor, w: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
     """a [T, K] . w [N, K]^T -> [T, N]: NVFP4 x NVFP4, MXFP4 x MXFP4, MXFP8 x MXFP4 or MXFP8 x MXFP8, scales tiled."""
-    device = _mx(a, "a")
-    _mx(w, "w", device)
-    d = _key(DTYPES, dtype, "dtype")
+    pa = _mx(a, "a")
+    device = pa[0]
+    pw = _mx(w, "w", device)
     if a.layout != "tiled" or w.layout != "tiled":
         raise ValueError("mx_matmul takes scales in the tiled layout (mx_tile_scales)")
     if a.K != w.K:
         raise ValueError(f"a has {a.K} columns, w {w.K}")
-    with _On(device, stream) as on:
-        if out is None:
-            out = torch.empty(a.rows, w.rows, dtype=dtype, device=device)
-        ld = _out(out, "out", (a.rows, w.rows), dtype, device)
-        _check(library().beam_mx_matmul(on.handle, FORMATS[a.format], _p(a.codes), _p(a.scales), _p(a.tensor_scale),
-                                        FORMATS[w.format], _p(w.codes), _p(w.scales), _p(w.tensor_scale),
-                                        a.rows, w.rows, a.K, _p(out), d, ld))
-        on.used(a.codes, a.scales, a.tensor_scale, w.codes, w.scales, w.tensor_scale, out)
-    return out
+    return _on(device, stream, _matmul, a, w, device, pa, pw, dtype, _key(DTYPES, dtype, "dtype"), out)
 
 
 # --- norm and routing ----------------------------------------------------------
+
+def _norm(handle, x, shape, gamma, residual, alpha, beta, eps, dtype, quantize, layout, out, residual_out, want_out,
+          quantized):
+    T, H, ldx, code = shape
+    device = x.device
+    d, lay = _key(DTYPES, dtype, "dtype"), _key(LAYOUTS, layout, "layout")
+    pr = pro = po = codes = scales = None
+    ldr = ldro = ldo = rd = 0
+    if residual is not None:
+        rt, rh, ldr, rd = _rows(residual, "residual", device)
+        if rt != T or rh != H or (rd != 2 and rd != code):
+            raise TypeError(f"residual: expected fp32 or {x.dtype} {(T, H)}, got {residual.dtype} {tuple(residual.shape)}")
+        if residual_out is None:
+            residual_out = torch.empty((T, H), dtype=residual.dtype, device=device)
+            ldro = H
+        else:
+            ldro = _out(residual_out, "residual_out", T, H, residual.dtype, device)
+        pr, pro = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if want_out:
+        if out is None:
+            out = torch.empty((T, H), dtype=dtype, device=device)
+            ldo = H
+        else:
+            ldo = _out(out, "out", T, H, dtype, device)
+        po = out.data_ptr()
+    elif out is not None:
+        raise ValueError("out given, but want_out is false")
+    if quantize is not None:
+        if quantize != "mxfp8":
+            raise ValueError(f"quantize: expected None or 'mxfp8', got {quantize!r}")
+        if quantized is None:
+            quantized = _new_mx(quantize, layout, T, H, device)
+            codes, scales = quantized.codes.data_ptr(), quantized.scales.data_ptr()
+        else:
+            codes, scales = _given_mx(quantized, "quantized", quantize, layout, T, H, device)
+    elif quantized is not None:
+        raise ValueError("quantized given, but quantize is None")
+    _check(library().beam_rms_norm(handle, x.data_ptr(), code, ldx, pr, rd, ldr, pro, ldro, alpha, beta,
+                                   _flat(gamma, "gamma", torch.float32, H, device), eps, T, H, po, d, ldo, codes, scales,
+                                   lay))
+    return NormResult(out, residual_out, quantized), (
+        x, gamma, residual, residual_out, out, *(() if quantized is None else quantized[:2]))
+
 
 def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, alpha: float = 1.0,
              beta: float = 1.0, eps: float = 1e-6, dtype=torch.bfloat16, quantize: Optional[str] = None,
@@ -292,48 +354,31 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tens
     residual s (None without residual; residual_out may be residual itself,
     to update it in place) and, with quantize="mxfp8", y as an MXFP8 operand.
     `out`, `residual_out`, `quantized`: buffers to write into."""
-    ldx = _rows(x, "x")
-    T, H = x.shape
-    device = x.device
-    _flat(gamma, "gamma", torch.float32, H, device)
-    d = _key(DTYPES, dtype, "dtype")
-    lay = _key(LAYOUTS, layout, "layout")
-    if quantize not in (None, "mxfp8"):
-        raise ValueError(f"quantize: expected None or 'mxfp8', got {quantize!r}")
-    ldr = ldro = ldo = 0
-    if residual is not None:
-        ldr = _rows(residual, "residual", device)
-        if tuple(residual.shape) != (T, H) or residual.dtype not in (torch.float32, x.dtype):
-            raise TypeError(f"residual: expected fp32 or {x.dtype} {(T, H)}, got {residual.dtype} {tuple(residual.shape)}")
-    elif residual_out is not None:
-        raise ValueError("residual_out without residual")
-    if out is not None and not want_out:
-        raise ValueError("out given, but want_out is false")
-    if quantized is not None and quantize is None:
-        raise ValueError("quantized given, but quantize is None")
-    with _On(device, stream) as on:
-        if residual is not None:
-            if residual_out is None:
-                residual_out = torch.empty(T, H, dtype=residual.dtype, device=device)
-            ldro = _out(residual_out, "residual_out", (T, H), residual.dtype, device)
-        if want_out:
-            if out is None:
-                out = torch.empty(T, H, dtype=dtype, device=device)
-            ldo = _out(out, "out", (T, H), dtype, device)
-        if quantize is not None:
-            if quantized is None:
-                quantized = _new_mx(quantize, layout, T, H, device)
-            else:
-                _mx(quantized, "quantized", device)
-                if (quantized.format, quantized.layout, quantized.rows, quantized.K) != (quantize, layout, T, H):
-                    raise ValueError(f"quantized: {quantized.format} {quantized.layout} {quantized.rows} x "
-                                     f"{quantized.K}, not {quantize} {layout} {T} x {H}")
-        codes, scales = (None, None) if quantized is None else (quantized.codes, quantized.scales)
-        _check(library().beam_rms_norm(
-            on.handle, _p(x), DTYPES[x.dtype], ldx, _p(residual), 0 if residual is None else DTYPES[residual.dtype],
-            ldr, _p(residual_out), ldro, alpha, beta, _p(gamma), eps, T, H, _p(out), d, ldo, _p(codes), _p(scales), lay))
-        on.used(x, gamma, residual, residual_out, out, codes, scales)
-    return NormResult(out, residual_out, quantized)
+    shape = _rows(x, "x")
+    return _on(x.device, stream, _norm, x, shape, gamma, residual, alpha, beta, eps, dtype, quantize, layout, out,
+               residual_out, want_out, quantized)
+
+
+def _route(handle, logits, shape, top_k, s, bias, n_group, topk_group, group_top, renormalize, scale, idx, w):
+    T, E, ld, code = shape
+    device = logits.device
+    if code != 2:
+        raise TypeError(f"logits: expected torch.float32, got {logits.dtype}")
+    k = top_k if top_k > 0 else 0      # refused below
+    if idx is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=device)
+        pi = idx.data_ptr()
+    else:
+        pi = _flat(idx, "idx", torch.int32, T * k, device)
+    if w is None:
+        w = torch.empty((T, k), dtype=torch.float32, device=device)
+        pw = w.data_ptr()
+    else:
+        pw = _flat(w, "w", torch.float32, T * k, device)
+    _check(library().beam_route_scores(handle, logits.data_ptr(), T, E, ld, s,
+                                       None if bias is None else _flat(bias, "bias", torch.float32, E, device), n_group,
+                                       topk_group, group_top, top_k, 1 if renormalize else 0, scale, pi, pw))
+    return (idx, w), (logits, bias, idx, w)
 
 
 def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias: Optional[torch.Tensor] = None,
@@ -346,21 +391,6 @@ def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias:
     the choice only; with topk_group < n_group the groups are ranked by the
     sum of their `group_top` best keys first.  A logit of -inf masks an
     expert; slots with no expert left get index -1, weight 0."""
-    _cuda(logits, "logits", torch.float32)
-    ld = _rows(logits, "logits")
-    T, E = logits.shape
-    device = logits.device
-    s = _key(SCORES, score, "score")
-    if bias is not None:
-        _flat(bias, "bias", torch.float32, E, device)
-    with _On(device, stream) as on:
-        if idx is None:
-            idx = torch.empty(T, max(top_k, 0), dtype=torch.int32, device=device)
-        if w is None:
-            w = torch.empty(T, max(top_k, 0), dtype=torch.float32, device=device)
-        _flat(idx, "idx", torch.int32, T * top_k, device)
-        _flat(w, "w", torch.float32, T * top_k, device)
-        _check(library().beam_route_scores(on.handle, _p(logits), T, E, ld, s, _p(bias), n_group, topk_group,
-                                           group_top, top_k, int(bool(renormalize)), scale, _p(idx), _p(w)))
-        on.used(logits, bias, idx, w)
-    return idx, w
+    shape = _rows(logits, "logits")
+    return _on(logits.device, stream, _route, logits, shape, top_k, _key(SCORES, score, "score"), bias, n_group,
+               topk_group, group_top, renormalize, scale, idx, w)

@@ -72,6 +72,10 @@ def test_route_reference_matches_torch_softmax():
 # --- refusals ----------------------------------------------------------------------
 
 def test_scale_bytes(lib):
+    for fmt, f in ops.FORMATS.items():
+        for layout, l in ops.LAYOUTS.items():
+            for rows in (0, 1, 128, 129, 1000):
+                assert ops.scale_bytes(fmt, rows, 96, layout) == lib.beam_mx_scale_bytes(f, rows, 96, l)
     assert lib.beam_mx_scale_bytes(0, 3, 64, 0) == 12
     assert lib.beam_mx_scale_bytes(0, 3, 64, 1) == 512
     assert lib.beam_mx_scale_bytes(0, 129, 80, 1) == 2 * 2 * 512
