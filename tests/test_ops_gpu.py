@@ -599,3 +599,36 @@ def test_bindings_refuse_mismatches():
         ops.rms_norm(x, torch.ones(64, device="cuda"), residual=x.half())
     with pytest.raises(ops.BeamMoEError):
         ops.route_scores(torch.zeros(2, 8, device="cuda"), 9)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep", [(64, 1, 1), (256, 8, 4), (480, 6, 2), (1000, 1, 1)])
+def test_route_many_experts_of_one_lane_and_ties_at_the_border(score, E, G, keep):
+    """The best experts side by side (one lane's whole list), and equal keys around the last place with a third one near."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(24, E, generator=g)
+    l[:8] = l[:8].sort(dim=1, descending=True).values
+    l[8:12] = l[8:12].sort(dim=1).values
+    l[12:16, :40] = 3.0                                # equal, more than are chosen
+    l[16:20, 5:12] = 3.0
+    l[20:22, 7:15] = 3.0
+    l[20:22, 15] = 3.0 + 2.0 ** -22                    # one ulp above the equal ones
+    l[22, :] = torch.linspace(2.0, 2.0 + 1e-5, E)
+    l = l.cuda()
+    bias = torch.randn(E, generator=g).cuda() * 1e-8
+    for k in (1, 8, 32):
+        for b in (None, torch.zeros(E, device="cuda"), bias):
+            for renorm in (False, True):
+                check_route(l, k, score, b, G, keep, 2, renorm)
+
+
+def test_route_long_batch_strided_rows():
+    """More rows than warps in flight, in rows off any vector alignment, against the same rows alone."""
+    l = torch.randn(9000, 256, generator=torch.Generator().manual_seed(2)).cuda()
+    bias = (torch.randn(256, generator=torch.Generator().manual_seed(3)) * 0.05).cuda()
+    want = ops.route_scores(l, 8, bias=bias, n_group=8, topk_group=4)
+    got = ops.route_scores(strided(l, 3), 8, bias=bias, n_group=8, topk_group=4)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    some = ops.route_scores(l[8500:8600], 8, bias=bias, n_group=8, topk_group=4)
+    assert torch.equal(some[0], want[0][8500:8600]) and torch.equal(some[1], want[1][8500:8600])
+    check_route(l[:700], 8, "sigmoid", bias, 8, 4)
