@@ -5,7 +5,9 @@
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (repo root) and
 linked, with the CUDA runtime statically, into
 ``group_limited_routing_sigmoid_b200/libbeam_moe.so``.  Objects are rebuilt
-when their source or any header is newer.
+when their source or any header is newer.  ``csrc/ops_binding.cpp``, the Python
+side of ``ops.py``, becomes ``_ops_binding.so`` beside it, with the host
+compiler against the installed PyTorch.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbeam_moe.so")
+OPS_BINDING = os.path.join(PKG, "_ops_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -37,6 +41,34 @@ def nvcc() -> str:
 
 def _newest(paths):
     return max(os.path.getmtime(p) for p in paths)
+
+
+def build_binding(force: bool = False, quiet: bool = False) -> str:
+    import torch    # its headers and libraries are compiled against
+
+    src = os.path.join(CSRC, "ops_binding.cpp")
+    stamp = os.path.join(BUILD, "ops_binding.torch")   # the version it was compiled against
+    known = os.path.exists(stamp) and open(stamp).read() == torch.__version__
+    if not force and known and os.path.exists(OPS_BINDING) and \
+            os.path.getmtime(OPS_BINDING) >= max(os.path.getmtime(src), _newest(glob.glob(os.path.join(INCLUDE, "*.h")))):
+        return OPS_BINDING
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = OPS_BINDING + f".tmp{os.getpid()}"
+    # the system's compiler: one that links its own libstdc++ statically would
+    # not catch PyTorch's exceptions
+    cmd = [shutil.which("g++") or os.environ.get("CXX", "c++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-o", tmp, src,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if not quiet:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, OPS_BINDING)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return OPS_BINDING
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
@@ -65,6 +97,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    build_binding(force, quiet)
     return LIB
 
 

@@ -2,12 +2,13 @@
 //
 // A warp per token.  With groups in play every group gets L lanes (a power of
 // two, L * n_group <= 32), else one group of 32; a lane owns `epl` consecutive
-// experts of its group, in registers.  A lane sorts its keys once (a network
-// of minima and maxima, no indexes carried); a group's best two are then the
-// heads of its lanes' lists, and each of the top_k rounds is one redux.max
-// over the 32 heads, a ballot for the lowest lane that holds it and a shift of
-// the winner's list.  The rounds' winners are turned into expert indexes
-// together at the end, lane j finding key j among its owner's keys.
+// experts of its group, in registers.  The choice is made among candidates: the
+// experts whose key reaches the n-th largest of the lanes' best keys (n the
+// experts wanted) hold the n largest and are few (about 13 of 256 for n = 9).
+// They are packed, one to a lane, and ranked by counting the larger ones.
+// 32768 x 256, 8 groups of which 4 stay, bias, top 8: 34 us (1.06 TB/s); without
+// groups and bias 22 us.  Lists sorted in the lanes with one maximum over their
+// heads per expert wanted took 49 and 26 us.
 //
 // Decisions are those of exact arithmetic: an FP32 score is off by a few
 // ulps, so a row in which two keys (neighbours of the chosen ranking) or two
@@ -15,8 +16,8 @@
 // exactly equal, is decided again from 64-bit scores (decide_row, the same
 // warp).  Without a bias the keys are the logits themselves, which are exact.
 //
-// Bound by instruction issue at large T (some 350 instructions a token of 256
-// grouped experts against 1 KB read), by the rounds' latency at small T.
+// Bound by instruction issue at large T, by the latency of a row's chain of
+// warp-wide steps at small T.
 #include "ops_common.cuh"
 
 namespace beam {
@@ -32,7 +33,7 @@ struct RouteArgs {
     float *w;
     long long ldl;
     int T, E;
-    int lanes;      // lanes a group (32 when no groups are dropped)
+    int lanes_log;  // log2 of the lanes a group has (5 when no groups are dropped)
     int size;       // experts a group (E when no groups are dropped)
     int epl;        // experts a lane
     int keep;       // groups that stay, 0: all
@@ -68,60 +69,32 @@ struct Span {
     int e0, mine;
     __device__ __forceinline__ Span(const RouteArgs &p, int lane)
     {
-        const int sub = (lane & (p.lanes - 1)) * p.epl, g = lane / p.lanes;
+        const int sub = (lane & ((1 << p.lanes_log) - 1)) * p.epl, g = lane >> p.lanes_log;
         e0 = g * p.size + sub;
         mine = e0 < p.E ? max(min(p.size - sub, p.epl), 0) : 0;
     }
 };
 
-// Sigmoid to about 2^-22 absolute: enough to rank by, with the margins below.
-__device__ __forceinline__ float sigmoid_fast(float x)
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    float e, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Sigmoid to about 2^-22 absolute: enough to rank by, with the margins below.
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -kLog2e)); }
+
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-
-// --- sorting in registers, descending -------------------------------------------
-
-__device__ __forceinline__ void order(float &a, float &b)
-{
-    const float hi = fmaxf(a, b);
-    b = fminf(a, b);
-    a = hi;
-}
-
-template <int N>
-__device__ __forceinline__ void sort(float *v)
-{
-    if constexpr (N == 2) {
-        order(v[0], v[1]);
-    } else if constexpr (N == 4) {
-        order(v[0], v[1]), order(v[2], v[3]), order(v[0], v[2]), order(v[1], v[3]), order(v[1], v[2]);
-    } else if constexpr (N == 8) {   // 19 comparisons
-        order(v[0], v[2]), order(v[1], v[3]), order(v[4], v[6]), order(v[5], v[7]);
-        order(v[0], v[4]), order(v[1], v[5]), order(v[2], v[6]), order(v[3], v[7]);
-        order(v[0], v[1]), order(v[2], v[3]), order(v[4], v[5]), order(v[6], v[7]);
-        order(v[2], v[4]), order(v[3], v[5]);
-        order(v[1], v[4]), order(v[3], v[6]);
-        order(v[1], v[2]), order(v[3], v[4]), order(v[5], v[6]);
-    }
-}
-
-// The eight largest of two sorted lists of eight, sorted, into a.
-__device__ __forceinline__ void merge8(float *a, const float *b)
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], b[7 - i]);   // bitonic
-#pragma unroll
-    for (int d = 4; d; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!(i & d)) order(a[i], a[i + d]);
-}
 
 // --- a row in 64 bits ------------------------------------------------------------
 
@@ -133,46 +106,44 @@ __device__ __noinline__ void decide_row(const RouteArgs &p, long long row)
     const int lane = threadIdx.x & 31;
     const Span my(p, lane);
     const float *l = p.logits + row * p.ldl;
-    double top = -INFINITY, log_sum = 0.0;
+    const int lanes = 1 << p.lanes_log;
+    double top = -INFINITY, sum = 1.0;
     double key[EPL];
     if (SOFTMAX) {
 #pragma unroll 1
         for (int i = 0; i < my.mine; ++i) top = fmax(top, (double)l[my.e0 + i]);
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
-        double sum = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < my.mine; ++i) sum += exp((double)l[my.e0 + i] - top);
-        log_sum = log(warp_sum(sum));
+        sum = 0.0;
     }
-    // log of the score of the expert with logit x
-    const auto log_score = [&](double x) {
-        return SOFTMAX ? x - top - log_sum : (x < 0 ? x - log1p(exp(x)) : -log1p(exp(-x)));
-    };
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        key[i] = -INFINITY;
-        if (i < my.mine) {
-            const double x = l[my.e0 + i];
-            const double b = BIAS ? (double)p.bias[my.e0 + i] : 0.0;
-            if (x > -INFINITY && b > -INFINITY) key[i] = exp(log_score(x)) + b;
-        }
+        const double x = i < my.mine ? (double)l[my.e0 + i] : -INFINITY;
+        key[i] = SOFTMAX ? exp(x - top) : 1.0 / (1.0 + exp(-x));
+        if (SOFTMAX) sum += key[i];
+    }
+    if (SOFTMAX) sum = warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const bool in = i < my.mine && l[my.e0 + i] > -INFINITY;
+        const double b = BIAS && in ? (double)p.bias[my.e0 + i] : 0.0;
+        key[i] = in ? (SOFTMAX ? key[i] / sum : key[i]) + b : -INFINITY;
     }
     bool kept = true;
     if (p.keep) {
         double a = -INFINITY, b = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) b = fmax(b, fmin(a, key[i])), a = fmax(a, key[i]);
-        for (int d = 1; d < p.lanes; d <<= 1) {
+        for (int d = 1; d < lanes; d <<= 1) {
             const double oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
             b = fmax(fmin(a, oa), fmax(b, ob));
             a = fmax(a, oa);
         }
         const double score = p.group_top == 2 && b > -INFINITY ? a + b : a;
         int rank = 0;
-        for (int g = 0; g < 32; g += p.lanes) {
+        for (int g = 0; g < 32; g += lanes) {
             const double o = __shfl_sync(0xffffffffu, score, g);
-            rank += o > score || (o == score && g < (lane & ~(p.lanes - 1)));
+            rank += o > score || (o == score && g < (lane & -lanes));
         }
         kept = rank < p.keep;
     }
@@ -202,7 +173,11 @@ __device__ __noinline__ void decide_row(const RouteArgs &p, long long row)
             if (my.e0 + i == at) key[i] = -INFINITY;
     }
     // weights from the logarithms, so that scores that underflow still share
-    const double my_log = my_idx >= 0 ? log_score(l[my_idx]) : -INFINITY;
+    double my_log = -INFINITY;
+    if (my_idx >= 0) {
+        const double x = l[my_idx];
+        my_log = SOFTMAX ? x - top - log(sum) : (x < 0 ? x - log1p(exp(x)) : -log1p(exp(-x)));
+    }
     double w = my_idx >= 0 ? exp(my_log) : 0.0;
     if (p.renorm) {
         double m = my_log;
@@ -223,17 +198,18 @@ __device__ __noinline__ void decide_row(const RouteArgs &p, long long row)
 template <int EPL, bool SOFTMAX, bool BIAS>
 __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scores_kernel(const RouteArgs p)
 {
-    // A lane's list holds its best eight; one that is used up in the rounds
-    // sends the row to decide_row.
-    constexpr int D = EPL < 8 ? EPL : 8;
-    __shared__ __align__(16) float s_keys[kRouteWarps][32 * EPL];
-    __shared__ float2 s_won[kRouteWarps][33];
+    __shared__ __align__(16) float s_key[kRouteWarps][36];   // candidates' keys, then the chosen order's
+    __shared__ int s_expert[kRouteWarps][32];
+    __shared__ float2 s_tie[kRouteWarps][BIAS ? 32 : 1];      // logit and bias in the chosen order
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t below = (1u << lane) - 1u;
     const Span my(p, lane);
-    float *keys = s_keys[warp];
-    float2 *won = s_won[warp];
+    float *cand = s_key[warp];
+    int *expert = s_expert[warp];
+    // with a bias one more than top_k: the best that is not chosen
+    const int want = BIAS ? p.top_k + 1 : p.top_k;
     float bias[BIAS ? EPL : 1];
     bool nan_bias = false;
     if constexpr (BIAS) {
@@ -247,22 +223,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
     for (long long row = (long long)blockIdx.x * kRouteWarps + warp; row < p.T;
          row += (long long)gridDim.x * kRouteWarps) {
         const float *l = p.logits + row * p.ldl;
-        float x[EPL];
+        float key[EPL];   // logits, then keys
         if (EPL % 4 == 0 && p.vec) {
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
                 const float4 v = i < my.mine ? *reinterpret_cast<const float4 *>(l + my.e0 + i)
                                              : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                x[i] = v.x;
-                if constexpr (EPL >= 4) x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                key[i] = v.x;
+                if constexpr (EPL >= 4) key[i + 1] = v.y, key[i + 2] = v.z, key[i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) x[i] = i < my.mine ? l[my.e0 + i] : -INFINITY;
+            for (int i = 0; i < EPL; ++i) key[i] = i < my.mine ? l[my.e0 + i] : -INFINITY;
         }
-        float top = x[0];
+        float top = key[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) top = max_nan(top, x[i]);
+        for (int i = 1; i < EPL; ++i) top = max_nan(top, key[i]);
+        float head = top;
         top = redux_max(top);
         if (top != top || (SOFTMAX && top == INFINITY) || nan_bias) {
             if (lane < p.top_k) {
@@ -273,51 +250,45 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
         }
         // softmax: the sum, where keys or weights need it
         float sum = 1.f;
-        float key[EPL];
-        if constexpr (SOFTMAX) {
-            if (BIAS || !p.renorm) {
+        const float ref = top > -INFINITY ? top : 0.f;
+        if constexpr (SOFTMAX && !BIAS) {
+            if (!p.renorm) {
                 sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) {
-                    key[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
-                    sum += key[i];
-                }
+                for (int i = 0; i < EPL; ++i) sum += exp2_fast((key[i] - ref) * kLog2e);
                 sum = warp_sum(sum);
             }
         }
-        const float inv = 1.0f / sum;   // the largest softmax score
+        if constexpr (BIAS) {
+            float inv = 1.f;
+            if constexpr (SOFTMAX) {
+                sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if constexpr (BIAS) {
-                const float k = (SOFTMAX ? key[i] * inv : sigmoid_fast(x[i])) + bias[i];
-                key[i] = x[i] > -INFINITY ? k : -INFINITY;
-            } else {
-                key[i] = x[i];
+                for (int i = 0; i < EPL; ++i) sum += exp2_fast((key[i] - ref) * kLog2e);
+                sum = warp_sum(sum);
+                inv = rcp_fast(sum);
+            }
+            head = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float s = SOFTMAX ? exp2_fast((key[i] - ref) * kLog2e) * inv : sigmoid_fast(key[i]);
+                key[i] = key[i] > -INFINITY ? s + bias[i] : -INFINITY;
+                head = fmaxf(head, key[i]);
             }
         }
         // How far two FP32 keys may be off together.  Sigmoid: 2^-22 each
         // (s(1-s) times the exponential's 2^-22 and its argument's rounding,
         // half an ulp of the sum, an ulp of the reciprocal).  Softmax: some
-        // ulps of the largest score each (exponential 2, its argument's
-        // rounding, 37 partial sums, two products).  And the rounding of the
-        // added bias.
-        const float tol_score = SOFTMAX ? 0x1p-19f * inv : 0x1p-20f;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) keys[lane * EPL + i] = key[i];
-        if constexpr (EPL == 16) {
-            sort<8>(key), sort<8>(key + 8);
-            merge8(key, key + 8);
-        } else if constexpr (EPL == 32) {
-            sort<8>(key), sort<8>(key + 8), sort<8>(key + 16), sort<8>(key + 24);
-            merge8(key, key + 8), merge8(key + 16, key + 24), merge8(key, key + 16);
-        } else {
-            sort<EPL>(key);
-        }
+        // ulps of the largest score 1 / sum each (exponential 2, its
+        // argument's rounding, 37 partial sums, two products).  And the
+        // rounding of the added bias.
+        const float tol_score = SOFTMAX ? 0x1p-19f * rcp_fast(sum) : 0x1p-20f;
         bool close = false;
         if (p.keep) {
-            float a = key[0], b = D > 1 ? key[D > 1 ? 1 : 0] : -INFINITY;
-            for (int d = 1; d < p.lanes; d <<= 1) {
+            float a = key[0], b = -INFINITY;
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) b = fmaxf(b, fminf(a, key[i])), a = fmaxf(a, key[i]);
+            for (int d = 1; d < 1 << p.lanes_log; d <<= 1) {
                 const float oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
                 b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                 a = fmaxf(a, oa);
@@ -329,12 +300,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
             }
             const float score = p.group_top == 2 && pb > -INFINITY ? pa + pb : pa;
             float left = score, lo = -INFINITY;
-            bool kept = false;
             for (int i = 0; i < p.keep; ++i) {
                 lo = redux_max(left);
-                if (lo == -INFINITY) break;
                 const int first = __ffs(__ballot_sync(0xffffffffu, left == lo)) - 1;   // a group's first lane
-                if ((lane & ~(p.lanes - 1)) == first) kept = true, left = -INFINITY;
+                if (lane >> p.lanes_log == first >> p.lanes_log) left = -INFINITY;
             }
             const float hi = redux_max(left);   // the best that is dropped
             const float tol = (BIAS ? 2.f * tol_score : 0x1p-19f) + 0x1p-21f * (fabsf(lo) + fabsf(hi));
@@ -349,78 +318,126 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
                     close = __any_sync(0xffffffffu, near && !(a == ta && (b == tb || p.group_top == 1)));
                 }
             }
-            if (!kept) key[0] = -INFINITY;
-        }
-        __syncwarp();
-        // with a bias one round more than top_k: the best that is not chosen
-        const int rounds = BIAS ? p.top_k + 1 : p.top_k;
-        int found = 0, popped = 0;
-        if (!close) {
-            for (; found < rounds; ++found) {
-                const float best = redux_max(key[0]);
-                if (best == -INFINITY) break;
-                const uint32_t m = __ballot_sync(0xffffffffu, key[0] == best);
-                if ((m & ((2u << lane) - 1u)) == (1u << lane)) {   // the lowest of them
-                    won[found] = make_float2(best, __int_as_float(lane));
+            if (left > -INFINITY) {   // dropped
+                head = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i + 1 < D; ++i) key[i] = key[i + 1];
-                    key[D - 1] = -INFINITY;
-                    if (EPL > D) ++popped;
-                }
+                for (int i = 0; i < EPL; ++i) key[i] = -INFINITY;
             }
-            if (EPL > D) close = __any_sync(0xffffffffu, popped >= D && my.mine > D);
         }
-        if (close) {
+        // candidates: keys of the want-th largest head and more (equal heads
+        // leave together, which only lowers the bound); -inf is none
+        float bound = -INFINITY;
+        for (int i = 0; i < want; ++i) {
+            bound = redux_max(head);
+            if (head == bound) head = -INFINITY;
+        }
+        bound = fmaxf(bound, -3.402823466e38f);
+        uint32_t has[EPL];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            has[i] = __ballot_sync(0xffffffffu, key[i] >= bound);
+            n += __popc(has[i]);
+        }
+        if (n > 32) {
+            // halve the gap up to the largest key, as integers of the floats'
+            // order, until at least `want` and at most 32 are left
+            const auto ordered = [](float v) {
+                const int b = __float_as_int(v);
+                return b < 0 ? b ^ 0x7fffffff : b;
+            };
+            float most = key[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) most = fmaxf(most, key[i]);
+            int low = ordered(bound), high = ordered(redux_max(most)) + 1;
+            for (int it = 0; it < 24 && n > 32; ++it) {
+                const int mid = low + (int)(((uint32_t)high - (uint32_t)low) >> 1);
+                const float v = __int_as_float(mid < 0 ? mid ^ 0x7fffffff : mid);
+                int m = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) m += __popc(__ballot_sync(0xffffffffu, key[i] >= v));
+                if (m < want) high = mid;
+                else low = mid, bound = v, n = m;
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) has[i] = __ballot_sync(0xffffffffu, key[i] >= bound);
+        }
+        if (close || n > 32) {
             decide_row<EPL, SOFTMAX, BIAS>(p, row);
             continue;
         }
-        __syncwarp();
-        // lane j: the expert of round j
-        const bool in = lane < found;
-        const float2 wj = won[in ? lane : 0];
-        const int owner = in ? __float_as_int(wj.y) : 0;
-        const float pk = __shfl_up_sync(0xffffffffu, wj.x, 1);
-        const int po = __shfl_up_sync(0xffffffffu, owner, 1);
-        const uint32_t repeat = __ballot_sync(0xffffffffu, in && lane > 0 && pk == wj.x && po == owner);
-        int at = 0;
-        if (repeat == 0u) {
+        __syncwarp();   // the last row's reads of cand
+        int base = 0;
 #pragma unroll
-            for (int i = EPL - 1; i >= 0; --i)
-                if (keys[owner * EPL + i] == wj.x) at = i;
-        } else {
-            // equal keys of one lane: the r-th of them in index order
-            int r = 0;
-            for (int j = lane; j > 0 && ((repeat >> j) & 1u); --j) ++r;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (keys[owner * EPL + i] == wj.x && r-- == 0) at = i;
+        for (int i = 0; i < EPL; ++i) {
+            if (has[i]) {
+                if ((has[i] >> lane) & 1u) {
+                    const int at = base + __popc(has[i] & below);
+                    cand[at] = key[i];
+                    expert[at] = my.e0 + i;
+                }
+                base += __popc(has[i]);
+            }
         }
-        const int e = owner / p.lanes * p.size + (owner & (p.lanes - 1)) * p.epl + at;
-        const float xe = in && found > 0 ? l[e] : -INFINITY;
+        if (lane < 4) cand[n + lane] = -INFINITY;   // whole fours below
+        __syncwarp();
+        const bool in = lane < n;
+        const float mine = cand[in ? lane : 0];
+        const int e = in ? expert[lane] : 0;
+        const float xe = in ? l[e] : -INFINITY;
+        int rank = 0;
+        for (int m = 0; m < n; m += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(cand + m);
+            rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        }
+        if (__popc(__reduce_or_sync(0xffffffffu, in ? 1u << rank : 0u)) != n) {
+            // equal keys: the lower index first
+            rank = 0;
+            for (int m = 0; m < n; ++m) rank += cand[m] > mine || (cand[m] == mine && expert[m] < e);
+        }
         if constexpr (BIAS) {
             // neighbours of the ranking too close to tell, unless their
-            // logits and biases are equal; an equal pair across the border
-            // may hide a third
+            // logits and biases are equal (across the border such a pair may
+            // hide a third); and the last chosen too close to what is no
+            // candidate
             const float be = in ? p.bias[e] : 0.f;
-            const float nk = lane + 1 < found ? won[lane + 1].x : -INFINITY;
-            const float nx = __shfl_down_sync(0xffffffffu, xe, 1), nb = __shfl_down_sync(0xffffffffu, be, 1);
-            const float tol = tol_score + 0x1p-22f * (fabsf(wj.x) + fabsf(nk));
-            const bool tied = nx == xe && nb == be && lane + 1 < p.top_k;
-            if (__any_sync(0xffffffffu, lane + 1 < found && !(wj.x - nk > tol) && !tied)) {
+            float2 *tie = s_tie[warp];
+            __syncwarp();
+            if (in) cand[rank] = mine, tie[rank] = make_float2(xe, be);
+            __syncwarp();
+            const bool check = lane < p.top_k && in;
+            const float k0 = check ? cand[lane] : 0.f;
+            const float k1 = check && lane + 1 < n ? cand[lane + 1] : bound;
+            const float tol = tol_score + 0x1p-22f * (fabsf(k0) + fabsf(k1));
+            const bool outside = check && lane == p.top_k - 1 && !(k0 - bound > tol);
+            const bool near = check && lane + 1 < n && !(k0 - k1 > tol) &&
+                              !(lane + 1 < p.top_k && tie[lane].x == tie[lane + 1].x && tie[lane].y == tie[lane + 1].y);
+            if (__any_sync(0xffffffffu, outside || (SOFTMAX && near))) {
                 decide_row<EPL, SOFTMAX, BIAS>(p, row);
                 continue;
             }
+            if (!SOFTMAX && __any_sync(0xffffffffu, near)) {
+                // all that may be chosen are candidates: rank those in 64 bits
+                const double exact = in ? 1.0 / (1.0 + exp(-(double)xe)) + (double)be : -INFINITY;
+                rank = 0;
+                for (int m = 0; m < n; ++m) {
+                    const double o = __shfl_sync(0xffffffffu, exact, m);
+                    const int oe = __shfl_sync(0xffffffffu, e, m);
+                    rank += o > exact || (o == exact && oe < e);
+                }
+            }
         }
-        const bool chosen = in && lane < p.top_k;
+        if (!in) rank = 32;
+        const bool chosen = rank < p.top_k;
         float w = 0.f;
         if constexpr (SOFTMAX) {
-            const float ref = p.renorm ? redux_max(chosen ? xe : -INFINITY) : top;
-            w = chosen ? expf(xe - ref) : 0.f;
+            const float most = p.renorm ? redux_max(chosen ? xe : -INFINITY) : top;
+            w = chosen ? expf(xe - most) : 0.f;
             if (!p.renorm && chosen) w = w / sum;
         } else {
             w = chosen ? sigmoid(xe) : 0.f;
         }
-        if (p.renorm && found > 0) {
+        if (p.renorm && n > 0) {
             const float s = warp_sum(w);
             if (!(s > 0x1p-90f)) {   // FP32 holds no full precision of it: from logarithms
                 decide_row<EPL, SOFTMAX, BIAS>(p, row);
@@ -428,9 +445,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
             }
             w = w / s;
         }
-        if (lane < p.top_k) {
-            p.idx[row * p.top_k + lane] = chosen ? e : -1;
-            p.w[row * p.top_k + lane] = w * p.scale;
+        if (chosen) {
+            p.idx[row * p.top_k + rank] = e;
+            p.w[row * p.top_k + rank] = w * p.scale;
+        }
+        if (lane >= n && lane < p.top_k) {   // no expert left
+            p.idx[row * p.top_k + lane] = -1;
+            p.w[row * p.top_k + lane] = 0.f;
         }
     }
 }
@@ -477,14 +498,16 @@ extern "C" int beam_route_scores(void *stream, const float *logits, int T, int E
     a.group_top = group_top, a.top_k = top_k, a.renorm = renormalize != 0, a.scale = scale;
     const bool groups = topk_group < n_group;
     a.keep = groups ? topk_group : 0;
-    a.lanes = 32;
-    while (groups && a.lanes * n_group > 32) a.lanes /= 2;
+    a.lanes_log = 5;
+    while (groups && n_group << a.lanes_log > 32) --a.lanes_log;
     a.size = groups ? E / n_group : E;
-    a.epl = (a.size + a.lanes - 1) / a.lanes;
+    a.epl = (a.size + (1 << a.lanes_log) - 1) >> a.lanes_log;
     if (a.epl > 2) a.epl = (a.epl + 3) / 4 * 4;   // whole 16-byte loads
     a.vec = a.size % 4 == 0 && a.epl % 4 == 0 && rows_aligned16(logits, ldl, BEAM_F32);
+    // twice the resident blocks: the second half starts where rows decided in
+    // 64 bits leave room (34 us; 38 with resident blocks only)
     const long long need = ((long long)T + kRouteWarps - 1) / kRouteWarps;
-    const dim3 grid((unsigned)(need < 4LL * sms ? need : 4LL * sms));
+    const dim3 grid((unsigned)(need < 8LL * sms ? need : 8LL * sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool softmax = score == BEAM_SCORE_SOFTMAX;
     cudaError_t e;

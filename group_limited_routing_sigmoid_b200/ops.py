@@ -8,19 +8,24 @@
 ``route_scores``  experts and weights from logits, softmax or sigmoid scores.
 
 Argument marshalling only, as in ``binding``: the work is the library's CUDA
-kernels; PyTorch supplies device memory and streams.  Every call runs on the
-device of its tensors, on ``stream`` or that device's current stream.  Where
-``stream`` is another one than the current stream, the caller orders the two
-for the inputs; outputs are made on ``stream`` and both are marked as used
-there.
+kernels; PyTorch supplies device memory and streams.  The checks of tensors
+and the outputs are made in ``csrc/ops_binding.cpp``, since they run beside
+kernels of a few microseconds.  Every call runs on the device of its tensors,
+on ``stream`` or that device's current stream.  Where ``stream`` is another
+one than the current stream, the caller orders the two for the inputs; outputs
+are made on ``stream`` and both are marked as used there.
 """
 from __future__ import annotations
 
+import ctypes
+import importlib.util
+import os
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from .binding import BEAM_ERR_INVALID_ARG, BEAM_OK, BeamMoEError, library
+from .binding import BEAM_ERR_INVALID_ARG, BeamMoEError, library
+from .build import OPS_BINDING
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
@@ -58,90 +63,44 @@ def _key(table, value, name):
     return code
 
 
-def _check(rc: int):
-    if rc != BEAM_OK:
-        raise BeamMoEError(rc, library().beam_ops_error().decode())
+_binding = None
 
 
-# The checks below run on every call, beside kernels of a few microseconds:
-# they read each property of a tensor once and take the common case first.
-
-def _bad_device(t, name: str, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor, got {t.device if isinstance(t, torch.Tensor) else type(t)}")
-    raise ValueError(f"{name}: on {t.device}, the others on {device}")
-
-
-def _rows(t, name: str, device=None):
-    """A matrix of a supported type on `device` (any CUDA device when None)
-    whose rows are contiguous -> (rows, columns, row stride, type code)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
-        _bad_device(t, name, device)
-    code = DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: expected one of {list(DTYPES)}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) == 2:
-        rows, cols = shape
-        if t.is_contiguous():
-            return rows, cols, cols, code
-        if cols <= 1 or t.stride(1) == 1:
-            ld = t.stride(0)
-            if rows <= 1:
-                return rows, cols, cols, code
-            if ld >= cols:
-                return rows, cols, ld, code
-            raise TypeError(f"{name}: rows overlap (stride {ld} for {cols} elements)")
-    raise TypeError(f"{name}: expected a matrix with contiguous rows, got shape {tuple(shape)}, strides {t.stride()}")
+def _native():
+    """The compiled binding, given the library's functions once (raises if either has not been built)."""
+    global _binding
+    if _binding is None:
+        lib = library()
+        if not os.path.exists(OPS_BINDING):
+            raise RuntimeError(f"{OPS_BINDING} is missing: build it with "
+                               "`python -m group_limited_routing_sigmoid_b200.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._ops_binding", OPS_BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(BeamMoEError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.beam_rms_norm, lib.beam_mx_tensor_scale, lib.beam_mx_quantize, lib.beam_mx_dequantize,
+            lib.beam_mx_tile_scales, lib.beam_mx_matmul, lib.beam_route_scores, lib.beam_ops_error)))
+        _binding = module
+    return _binding
 
 
-def _flat(t, name: str, dtype, n: int, device):
-    """A contiguous tensor of n elements of `dtype` on `device` -> its address."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        _bad_device(t, name, device)
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise TypeError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)} "
-                        f"(contiguous={t.is_contiguous()})")
-    return t.data_ptr()
-
-
-def _out(t, name: str, rows: int, cols: int, dtype, device) -> int:
-    """An output matrix the caller gave -> its row stride."""
-    r, c, ld, _ = _rows(t, name, device)
-    if r != rows or c != cols or t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype} {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
-    return ld
-
-
-# The current stream's handle without a Stream object around it, where torch has that.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _on(device, stream, body, *args):
-    """body(stream handle, *args) on `device` and `stream` (None: the device's
-    current stream).  body returns (result, tensors it uses): those are made
-    on that stream and, where it is another one than the current stream,
-    marked as used there."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(_raw_stream(device.index), *args)[0]
+def _elsewhere(stream, f, *args):
+    """f(*args) on `stream` of the first argument's device, all tensors marked as used there."""
+    if not isinstance(args[0], torch.Tensor) or not args[0].is_cuda:
+        return f(*args)                # which refuses it
+    device = args[0].device
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
     with torch.cuda.device(device):
-        current = _raw_stream(device.index)
-        if stream is None:
-            return body(current, *args)[0]
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if handle == current:
-            return body(current, *args)[0]
+        if handle == torch.cuda.current_stream(device).cuda_stream:
+            return f(*args)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(handle, device=device)
-        if stream.device != device:
-            raise ValueError(f"stream on {stream.device}, tensors on {device}")
         with torch.cuda.stream(stream):
-            result, tensors = body(handle, *args)
-        for t in tensors:
-            if t is not None:
+            result = f(*args)
+        for t in (*args, *(result if isinstance(result, tuple) else (result,))):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(stream)
         return result
 
@@ -149,7 +108,10 @@ def _on(device, stream, body, *args):
 def ops_status(device=None, stream=None) -> int:
     """Wait for `stream`, then read and clear the device's status word."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _on(device, stream, lambda handle: (library().beam_ops_status(handle), ()))
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        return library().beam_ops_status(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
 # --- microscaled operands ------------------------------------------------------
@@ -166,68 +128,26 @@ def scale_bytes(format: str, rows: int, K: int, layout: str) -> int:
     return rows * n if layout == "rows" else (rows + 127) // 128 * ((n + 3) // 4) * 512
 
 
-def _new_mx(format: str, layout: str, rows: int, K: int, device) -> MxTensor:
-    n = scale_bytes(format, rows, K, layout)
-    codes = torch.empty((rows, K if format == "mxfp8" else K // 2), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, K // BLOCK[format]) if layout == "rows" else n, dtype=torch.uint8, device=device)
-    return MxTensor(codes, scales, format, layout, rows, K)
-
-
-def _mx(q: MxTensor, name: str, device=None):
-    """Types, sizes and device of an operand's tensors -> (device, addresses of codes, scales, tensor scale)."""
+def _operand(q, name: str):
+    """Fields of an operand: codes, scales, tensor scale, codes of its format and layout, rows, K."""
     if not isinstance(q, MxTensor):
         raise TypeError(f"{name}: expected an MxTensor, got {type(q)}")
-    codes, scales, fmt, layout, rows, K, ts = q
-    n = scale_bytes(fmt, rows, K, layout)
-    if device is None:
-        if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
-            _bad_device(codes, name + ".codes", device)
-        device = codes.device
-    return (device, _flat(codes, name, torch.uint8, rows * (K if fmt == "mxfp8" else K // 2), device),
-            _flat(scales, name, torch.uint8, n, device),
-            None if ts is None else _flat(ts, name, torch.float32, 1, device))
+    codes, scales, format, layout, rows, K, tensor_scale = q
+    return codes, scales, tensor_scale, _key(FORMATS, format, name), _key(LAYOUTS, layout, name), rows, K
 
 
-def _given_mx(q: MxTensor, name: str, format: str, layout: str, rows: int, K: int, device):
-    """An operand to write into: of this format, layout and shape -> addresses of codes, scales."""
-    _, codes, scales, _ = _mx(q, name, device)
-    if (q.format, q.layout, q.rows, q.K) != (format, layout, rows, K):
-        raise ValueError(f"{name}: {q.format} {q.layout} {q.rows} x {q.K}, not {format} {layout} {rows} x {K}")
+def _given(q, name: str, format: str, layout: str, x):
+    """Codes and scales of an operand to write into: of this format and layout and x's shape."""
+    codes, scales, _, _, _, rows, K = _operand(q, name)
+    if (q.format, q.layout, rows, K) != (format, layout, *x.shape):
+        raise ValueError(f"{name}: {q.format} {q.layout} {rows} x {K}, not {format} {layout} {tuple(x.shape)}")
     return codes, scales
-
-
-def _tensor_scale(handle, x, shape, out):
-    if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
-    rows, K, ld, code = shape
-    _check(library().beam_mx_tensor_scale(handle, x.data_ptr(), code, rows, K, ld,
-                                          _flat(out, "out", torch.float32, 1, x.device)))
-    return out, (x, out)
 
 
 def mx_tensor_scale(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The NVFP4 scale of x [rows, K]: the least power of two g with amax <= 6 * 448 * g (fp32 [1])."""
-    return _on(x.device, stream, _tensor_scale, x, _rows(x, "x"), out)
-
-
-def _quantize(handle, x, shape, format, f, layout, lay, tensor_scale, out):
-    rows, K, ld, code = shape
-    device = x.device
-    if out is None:
-        out = _new_mx(format, layout, rows, K, device)
-        codes, scales = out.codes.data_ptr(), out.scales.data_ptr()
-    else:
-        codes, scales = _given_mx(out, "out", format, layout, rows, K, device)
-    ts = None
-    if f == 0:
-        if tensor_scale is None:
-            tensor_scale, _ = _tensor_scale(handle, x, shape, None)
-        ts = _flat(tensor_scale, "tensor_scale", torch.float32, 1, device)
-    elif tensor_scale is not None:
-        raise ValueError(f"{format} has no tensor scale")
-    _check(library().beam_mx_quantize(handle, x.data_ptr(), code, rows, K, ld, f, lay, ts, codes, scales))
-    out = MxTensor(out.codes, out.scales, format, layout, rows, K, tensor_scale)
-    return out, (x, tensor_scale, out.codes, out.scales)
+    f = (_binding or _native()).tensor_scale
+    return f(x, out) if stream is None else _elsewhere(stream, f, x, out)
 
 
 def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale: Optional[torch.Tensor] = None,
@@ -238,110 +158,50 @@ def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale
     one more pass over x).  layout "rows" is what BeamMoE.nvfp4 and checkpoints
     take, "tiled" what mx_matmul takes.  `out`: an operand of the same shape to
     write into (its tensor_scale is not)."""
-    return _on(x.device, stream, _quantize, x, _rows(x, "x"), format, _key(FORMATS, format, "format"), layout,
-               _key(LAYOUTS, layout, "layout"), tensor_scale, out)
-
-
-def _dequantize(handle, q, device, codes, scales, ts, dtype, d, out):
-    if out is None:
-        out = torch.empty((q.rows, q.K), dtype=dtype, device=device)
-        ld = q.K
-    else:
-        ld = _out(out, "out", q.rows, q.K, dtype, device)
-    _check(library().beam_mx_dequantize(handle, codes, scales, ts, FORMATS[q.format], LAYOUTS[q.layout], q.rows, q.K,
-                                        out.data_ptr(), d, ld))
-    return out, (q.codes, q.scales, q.tensor_scale, out)
+    f, lay = _key(FORMATS, format, "format"), _key(LAYOUTS, layout, "layout")
+    codes, scales = (None, None) if out is None else _given(out, "out", format, layout, x)
+    if f != 0 and tensor_scale is not None:
+        raise ValueError(f"{format} has no tensor scale")
+    q = (_binding or _native()).quantize
+    codes, scales, tensor_scale, rows, K = (
+        q(x, f, lay, tensor_scale, codes, scales) if stream is None else
+        _elsewhere(stream, q, x, f, lay, tensor_scale, codes, scales))
+    return MxTensor(codes, scales, format, layout, rows, K, tensor_scale)
 
 
 def mx_dequantize(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of a microscaled operand, [rows, K]."""
-    device, codes, scales, ts = _mx(q, "q")
-    return _on(device, stream, _dequantize, q, device, codes, scales, ts, dtype, _key(DTYPES, dtype, "dtype"), out)
-
-
-def _tile(handle, q, device, scales):
-    tiled = torch.empty(scale_bytes(q.format, q.rows, q.K, "tiled"), dtype=torch.uint8, device=device)
-    _check(library().beam_mx_tile_scales(handle, FORMATS[q.format], scales, q.rows, q.K, tiled.data_ptr()))
-    return q._replace(scales=tiled, layout="tiled"), (q.scales, tiled)
+    args = (*_operand(q, "q"), _key(DTYPES, dtype, "dtype"), out)
+    f = (_binding or _native()).dequantize
+    return f(*args) if stream is None else _elsewhere(stream, f, *args)
 
 
 def mx_tile_scales(q: MxTensor, stream=None) -> MxTensor:
     """The same operand with its scales in the "tiled" layout (once, for a checkpoint's weights)."""
-    device, _, scales, _ = _mx(q, "q")
-    return q if q.layout == "tiled" else _on(device, stream, _tile, q, device, scales)
-
-
-def _matmul(handle, a, w, device, pa, pw, dtype, d, out):
-    T, N = a.rows, w.rows
-    if out is None:
-        out = torch.empty((T, N), dtype=dtype, device=device)
-        ld = N
-    else:
-        ld = _out(out, "out", T, N, dtype, device)
-    _check(library().beam_mx_matmul(handle, FORMATS[a.format], pa[1], pa[2], pa[3], FORMATS[w.format], pw[1], pw[2],
-                                    pw[3], T, N, a.K, out.data_ptr(), d, ld))
-    return out, (a.codes, a.scales, a.tensor_scale, w.codes, w.scales, w.tensor_scale, out)
+    _, scales, _, format, _, rows, K = _operand(q, "q")
+    if q.layout == "tiled":
+        return q
+    f = (_binding or _native()).tile_scales
+    tiled = f(scales, format, rows, K) if stream is None else _elsewhere(stream, f, scales, format, rows, K)
+    return q._replace(scales=tiled, layout="tiled")
 
 
 def mx_matmul(a: MxTensor, w: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
     """a [T, K] . w [N, K]^T -> [T, N]: NVFP4 x NVFP4, MXFP4 x MXFP4, MXFP8 x MXFP4 or MXFP8 x MXFP8, scales tiled."""
-    pa = _mx(a, "a")
-    device = pa[0]
-    pw = _mx(w, "w", device)
-    if a.layout != "tiled" or w.layout != "tiled":
+    ac, asc, ag, af, al, T, K = _operand(a, "a")
+    wc, wsc, wg, wf, wl, N, wk = _operand(w, "w")
+    if al != 1 or wl != 1:
         raise ValueError("mx_matmul takes scales in the tiled layout (mx_tile_scales)")
-    if a.K != w.K:
-        raise ValueError(f"a has {a.K} columns, w {w.K}")
-    return _on(device, stream, _matmul, a, w, device, pa, pw, dtype, _key(DTYPES, dtype, "dtype"), out)
+    if K != wk:
+        raise ValueError(f"a has {K} columns, w {wk}")
+    f = (_binding or _native()).matmul
+    d = _key(DTYPES, dtype, "dtype")
+    return (f(ac, asc, ag, af, wc, wsc, wg, wf, T, N, K, d, out) if stream is None else
+            _elsewhere(stream, f, ac, asc, ag, af, wc, wsc, wg, wf, T, N, K, d, out))
 
 
 # --- norm and routing ----------------------------------------------------------
-
-def _norm(handle, x, shape, gamma, residual, alpha, beta, eps, dtype, quantize, layout, out, residual_out, want_out,
-          quantized):
-    T, H, ldx, code = shape
-    device = x.device
-    d, lay = _key(DTYPES, dtype, "dtype"), _key(LAYOUTS, layout, "layout")
-    pr = pro = po = codes = scales = None
-    ldr = ldro = ldo = rd = 0
-    if residual is not None:
-        rt, rh, ldr, rd = _rows(residual, "residual", device)
-        if rt != T or rh != H or (rd != 2 and rd != code):
-            raise TypeError(f"residual: expected fp32 or {x.dtype} {(T, H)}, got {residual.dtype} {tuple(residual.shape)}")
-        if residual_out is None:
-            residual_out = torch.empty((T, H), dtype=residual.dtype, device=device)
-            ldro = H
-        else:
-            ldro = _out(residual_out, "residual_out", T, H, residual.dtype, device)
-        pr, pro = residual.data_ptr(), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out without residual")
-    if want_out:
-        if out is None:
-            out = torch.empty((T, H), dtype=dtype, device=device)
-            ldo = H
-        else:
-            ldo = _out(out, "out", T, H, dtype, device)
-        po = out.data_ptr()
-    elif out is not None:
-        raise ValueError("out given, but want_out is false")
-    if quantize is not None:
-        if quantize != "mxfp8":
-            raise ValueError(f"quantize: expected None or 'mxfp8', got {quantize!r}")
-        if quantized is None:
-            quantized = _new_mx(quantize, layout, T, H, device)
-            codes, scales = quantized.codes.data_ptr(), quantized.scales.data_ptr()
-        else:
-            codes, scales = _given_mx(quantized, "quantized", quantize, layout, T, H, device)
-    elif quantized is not None:
-        raise ValueError("quantized given, but quantize is None")
-    _check(library().beam_rms_norm(handle, x.data_ptr(), code, ldx, pr, rd, ldr, pro, ldro, alpha, beta,
-                                   _flat(gamma, "gamma", torch.float32, H, device), eps, T, H, po, d, ldo, codes, scales,
-                                   lay))
-    return NormResult(out, residual_out, quantized), (
-        x, gamma, residual, residual_out, out, *(() if quantized is None else quantized[:2]))
-
 
 def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, alpha: float = 1.0,
              beta: float = 1.0, eps: float = 1e-6, dtype=torch.bfloat16, quantize: Optional[str] = None,
@@ -354,31 +214,25 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tens
     residual s (None without residual; residual_out may be residual itself,
     to update it in place) and, with quantize="mxfp8", y as an MXFP8 operand.
     `out`, `residual_out`, `quantized`: buffers to write into."""
-    shape = _rows(x, "x")
-    return _on(x.device, stream, _norm, x, shape, gamma, residual, alpha, beta, eps, dtype, quantize, layout, out,
-               residual_out, want_out, quantized)
-
-
-def _route(handle, logits, shape, top_k, s, bias, n_group, topk_group, group_top, renormalize, scale, idx, w):
-    T, E, ld, code = shape
-    device = logits.device
-    if code != 2:
-        raise TypeError(f"logits: expected torch.float32, got {logits.dtype}")
-    k = top_k if top_k > 0 else 0      # refused below
-    if idx is None:
-        idx = torch.empty((T, k), dtype=torch.int32, device=device)
-        pi = idx.data_ptr()
-    else:
-        pi = _flat(idx, "idx", torch.int32, T * k, device)
-    if w is None:
-        w = torch.empty((T, k), dtype=torch.float32, device=device)
-        pw = w.data_ptr()
-    else:
-        pw = _flat(w, "w", torch.float32, T * k, device)
-    _check(library().beam_route_scores(handle, logits.data_ptr(), T, E, ld, s,
-                                       None if bias is None else _flat(bias, "bias", torch.float32, E, device), n_group,
-                                       topk_group, group_top, top_k, 1 if renormalize else 0, scale, pi, pw))
-    return (idx, w), (logits, bias, idx, w)
+    codes = scales = None
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if not want_out and out is not None:
+        raise ValueError("out given, but want_out is false")
+    if quantize is not None and quantize != "mxfp8":
+        raise ValueError(f"quantize: expected None or 'mxfp8', got {quantize!r}")
+    if quantized is not None:
+        if quantize is None:
+            raise ValueError("quantized given, but quantize is None")
+        codes, scales = _given(quantized, "quantized", quantize, layout, x)
+    f = (_binding or _native()).rms_norm
+    d, lay = _key(DTYPES, dtype, "dtype"), _key(LAYOUTS, layout, "layout")
+    args = (x, gamma, residual, alpha, beta, eps, d, quantize is not None, lay, out, residual_out, bool(want_out), codes,
+            scales)
+    out, residual_out, codes, scales, T, H = f(*args) if stream is None else _elsewhere(stream, f, *args)
+    if quantize is None:
+        return NormResult(out, residual_out, None)
+    return NormResult(out, residual_out, MxTensor(codes, scales, quantize, layout, T, H))
 
 
 def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias: Optional[torch.Tensor] = None,
@@ -391,6 +245,8 @@ def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias:
     the choice only; with topk_group < n_group the groups are ranked by the
     sum of their `group_top` best keys first.  A logit of -inf masks an
     expert; slots with no expert left get index -1, weight 0."""
-    shape = _rows(logits, "logits")
-    return _on(logits.device, stream, _route, logits, shape, top_k, _key(SCORES, score, "score"), bias, n_group,
-               topk_group, group_top, renormalize, scale, idx, w)
+    s = _key(SCORES, score, "score")
+    f = (_binding or _native()).route_scores
+    if stream is None:
+        return f(logits, top_k, s, bias, n_group, topk_group, group_top, renormalize, scale, idx, w)
+    return _elsewhere(stream, f, logits, top_k, s, bias, n_group, topk_group, group_top, renormalize, scale, idx, w)
