@@ -1,12 +1,21 @@
 // Microscaled operands (beam_mx_*): making them from 16- or 32-bit rows,
 // reading them back, and laying their scales out for the tensor cores.
 //
-// All of it is bound by HBM: a 16-bit element is 2 bytes in and 0.53 to 1.03
-// out.  A warp takes 256 consecutive elements of a row, 8 a lane (one 16-byte
-// load of 16-bit elements); a block of 16 or 32 elements is 2 or 4
-// neighbouring lanes, whose largest magnitude is found by shuffles.  Where
-// rows are contiguous and the scales lie row by row, the whole tensor is
-// taken as one row (blocks divide rows, so they do not notice).
+// Bound by HBM: a 16-bit element is 2 bytes in and 0.53 to 1.03 out.  A lane
+// takes 16 consecutive elements of a row (a 32-byte load of 16-bit ones): an
+// NVFP4 block is one lane's, a block of 32 two neighbouring lanes', whose
+// largest magnitude meets in one shuffle.  Chunks of 16 are numbered through
+// all rows, so short rows fill warps as well as long ones; where rows are
+// contiguous and the scales lie row by row, the whole tensor is one row.  Two
+// chunks a lane are loaded before either is worked on.  Quotients go two an
+// instruction (fma.rn.f32x2), else NVFP4 is bound by issue.  Chunks are taken
+// from the last to the first: what a kernel before this one touched last (the
+// tensor scale's pass, the producer's stores) is still in L2.
+//
+// 20480 x 5120 bf16 on a B200: tensor scale 35 us (6.0 TB/s), NVFP4 46 us
+// (5.8 TB/s; tiled scales 55 us), MXFP8 tiled 53 us (6.0 TB/s), NVFP4 back to
+// bf16 45 to 48 us (5.6 to 6.0 TB/s).  With 8 elements a lane, one load ahead
+// and scalar arithmetic the first two and the last took 195 us together, now 133.
 #include "ops_common.cuh"
 
 namespace beam {
@@ -14,12 +23,40 @@ namespace {
 
 using namespace ops;
 
-constexpr int kWarps = 8;          // warps a block
-constexpr int kUnit = 256;         // elements a warp takes at a time
+constexpr int kThreadsQ = 256;
+constexpr int kChunk = 16;         // elements a lane takes at a time
+constexpr int kAhead = 2;          // chunks a lane loads at once
 
 // NVFP4 tensor scales outside this range would leave the exact range of the
 // arithmetic below (block scale * tensor scale, its reciprocal, residuals).
 constexpr float kMinTensorScale = 0x1p-112f, kMaxTensorScale = 0x1p112f;
+
+// Chunk number -> row and chunk in the row.  Numbers stay below 2^31: larger
+// tensors go in slices of rows (kSlice chunks, or a row where that has more).
+constexpr long long kSlice = 1ll << 27;
+
+struct Chunks {
+    uint32_t magic;   // ceil(2^(31 + s) / per_row), s = ceil(log2 per_row)
+    int shift;        // s - 1
+    int total, per_row;
+    Chunks() = default;
+    Chunks(int rows, int per) : magic(0), shift(0), total(rows * per), per_row(per)
+    {
+        if (per <= 1) return;
+        while ((1ll << (shift + 1)) < per) ++shift;
+        magic = (uint32_t)(((1ull << (32 + shift)) + (unsigned long long)per - 1) / (unsigned long long)per);
+    }
+    template <int AL>
+    __device__ __forceinline__ void at(int c, int &row, int &in_row) const
+    {
+        if constexpr (AL == 64) {   // kFlat
+            row = 0, in_row = c;
+        } else {
+            row = per_row == 1 ? c : (int)(__umulhi((uint32_t)c, magic) >> shift);
+            in_row = c - row * per_row;
+        }
+    }
+};
 
 struct QuantArgs {
     const void *x;
@@ -27,10 +64,137 @@ struct QuantArgs {
     uint8_t *codes, *scales;
     long long rows, ldx;    // rows of the tensor (or 1)
     long long K;            // elements a row
-    long long units;        // warp units: rows (padded to the tile) x units a row
-    long long units_row;
+    long long row0;         // first row of this slice
+    Chunks chunks;
     ScaleMap map;
 };
+
+// How chunks lie: kFlat, one row of 32-byte aligned chunks (no division, no
+// row strides: 20480 x 5120 to NVFP4 52 us, 59 without), else the alignment
+// known of every chunk in bytes (32, 16, or 0: the element's).
+constexpr int kFlat = 64;
+
+// Sixteen consecutive elements.
+template <typename T> struct Raw16 { uint32_t w[4 * sizeof(T)]; };
+
+template <int AL, typename T>
+__device__ __forceinline__ Raw16<T> load_raw16(const T *p)
+{
+    Raw16<T> r;
+    if constexpr (AL >= 32) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.w[8 * i]), "=r"(r.w[8 * i + 1]), "=r"(r.w[8 * i + 2]), "=r"(r.w[8 * i + 3]),
+                           "=r"(r.w[8 * i + 4]), "=r"(r.w[8 * i + 5]), "=r"(r.w[8 * i + 6]), "=r"(r.w[8 * i + 7])
+                         : "l"(reinterpret_cast<const uint32_t *>(p) + 8 * i));
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const Raw8<T> v = load_raw8<AL == 16>(p + 8 * h);
+#pragma unroll
+            for (int i = 0; i < (int)(2 * sizeof(T)); ++i) r.w[h * 2 * sizeof(T) + i] = v.w[i];
+        }
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const Raw16<T> &r, float (&v)[16])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        Raw8<T> q;
+#pragma unroll
+        for (int i = 0; i < (int)(2 * sizeof(T)); ++i) q.w[i] = r.w[h * 2 * sizeof(T) + i];
+        float f[8];
+        unpack8(q, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = f[i];
+    }
+}
+
+// Largest magnitude of the chunk as the bits of a float (NaN above infinity
+// above every finite value).  16-bit types are compared in pairs, in their own
+// bits: their order is that of the floats.
+template <typename T>
+__device__ __forceinline__ uint32_t amax_bits16(const Raw16<T> &r)
+{
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, r.w[i] & 0x7fffffffu);
+        return m;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, r.w[i] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    }
+}
+
+template <int AL, typename T>
+__device__ __forceinline__ void store16(T *p, const float (&v)[16])
+{
+    if constexpr (AL >= 32) {
+        uint32_t w[4 * sizeof(T)];
+#pragma unroll
+        for (int i = 0; i < (int)(4 * sizeof(T)); ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+            else if constexpr (std::is_same<T, __nv_bfloat16>::value) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            else w[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             reinterpret_cast<uint32_t *>(p) + 8 * i),
+                         "r"(w[8 * i]), "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
+                         "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = v[8 * h + i];
+            store8<AL == 16>(p + 8 * h, f);
+        }
+    }
+}
+
+__device__ __forceinline__ const float (&half_of(const float (&v)[16], int h))[8]
+{
+    return *reinterpret_cast<const float(*)[8]>(v + 8 * h);
+}
+
+// Two FP32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ void scale16(float (&v)[16], float s)
+{
+    const uint64_t ss = pair(s, s);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) unpair(mul2(pair(v[i], v[i + 1]), ss), v[i], v[i + 1]);
+}
 
 // x / d correctly rounded, from r = 1/d rounded: one step of Markstein's
 // residual correction (IBM J. Res. Dev. 34, 1990).  Ties of the 4-bit grid
@@ -41,73 +205,106 @@ __device__ __forceinline__ float quotient(float x, float d, float r)
     return fmaf(fmaf(-q, d, x), r, q);
 }
 
-// One unit: 8 elements a lane, at element k of `row`.  `live`: the elements
-// exist; otherwise only a scale byte past the end may have to be zeroed.
-template <typename T, int FMT>
-__device__ __forceinline__ void quantize_unit(const QuantArgs &p, const Raw8<T> &raw, long long row,
-                                              long long k, bool live, int lane, float g)
+// The same for sixteen.
+__device__ __forceinline__ void quotient16(float (&v)[16], float d, float r)
 {
-    float v[8];
-    uint32_t m = 0;
-    if (live) {
-        unpack8(raw, v);
-        m = amax_bits8(v);
-    }
-    constexpr int GROUP = FMT == BEAM_NVFP4 ? 2 : 4;
+    const uint64_t rr = pair(r, r), nd = pair(-d, -d);
 #pragma unroll
-    for (int d = 1; d < GROUP; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    bool bad = m >= kInfBits;
+    for (int i = 0; i < 16; i += 2) {
+        const uint64_t x = pair(v[i], v[i + 1]), q = mul2(x, rr);
+        unpair(fma2(fma2(q, nd, x), rr, q), v[i], v[i + 1]);
+    }
+}
+
+// One chunk of a row, at element k.  `live`: the elements exist; otherwise
+// only a scale byte past the end may have to be zeroed.  Whole warps call it.
+template <typename T, int FMT, int AL>
+__device__ __forceinline__ void quantize_chunk(const QuantArgs &p, const Raw16<T> &raw, long long row, long long k,
+                                               bool live, float g, float r6)
+{
+    uint32_t m = amax_bits16(raw);
+    if constexpr (FMT != BEAM_NVFP4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float v[16];
+    unpack16(raw, v);
+    const bool bad = m >= kInfBits || (FMT == BEAM_NVFP4 && !(g >= kMinTensorScale && g <= kMaxTensorScale));
     uint32_t sb;
     if constexpr (FMT == BEAM_NVFP4) {
-        bad |= !(g >= kMinTensorScale && g <= kMaxTensorScale);
-        sb = bad ? 0x7fu : e4m3_byte(__uint_as_float(m) / (6.0f * g));
+        // amax / (6 g), correctly rounded where it is below the largest scale
+        float q = __uint_as_float(m) * r6;
+        if (q < 512.f) q = quotient(__uint_as_float(m), 6.0f * g, r6);
+        sb = bad ? 0x7fu : e4m3_byte(q);
         const float d = e4m3x2_values(sb).x * g;
         const float r = 1.0f / d;
-        const bool zero = bad || sb == 0;
-        // a block whose scale saturated (a tensor scale found on other data):
-        // its large quotients only have to stay large, and may be infinite
-        const bool over = !(__uint_as_float(m) * r < 8.0f);
+        if (bad || sb == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = over ? v[i] * r : quotient(v[i], d, r);
-            v[i] = zero ? 0.f : q;
+            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        } else if (!(__uint_as_float(m) * r < 8.0f)) {
+            // the scale saturated (a tensor scale found on other data): large
+            // quotients only have to stay large, and may be infinite
+            scale16(v, r);
+        } else {
+            quotient16(v, d, r);
         }
     } else {
         constexpr uint32_t TOP = FMT == BEAM_MXFP4 ? kTop6 : kTop448;
         sb = bad ? 0xffu : ue8m0_byte<TOP>(__uint_as_float(m));
-        const float inv = bad ? 0.f : ue8m0_inverse(sb);
+        if (bad) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = bad ? 0.f : v[i] * inv;
+            for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        } else {
+            scale16(v, ue8m0_inverse(sb));
+        }
     }
+    const long long j = k / block_size(FMT);
+    const bool first = FMT == BEAM_NVFP4 || (k & 16) == 0;
     if (live) {
-        const size_t at = (size_t)row * p.K + k;
-        if constexpr (FMT == BEAM_MXFP8) *reinterpret_cast<uint2 *>(p.codes + at) = e4m3x8(v);
-        else *reinterpret_cast<uint32_t *>(p.codes + at / 2) = e2m1x8(v);
-    }
-    constexpr int BLOCK = 8 * GROUP;
-    const long long j = k / BLOCK;
-    if ((lane & (GROUP - 1)) == 0) {
-        if (live) p.scales[p.map.at(row, j)] = (uint8_t)sb;
-        else if (p.map.tiled && j < 4 * p.map.n4) p.scales[p.map.at(row, j)] = 0;
+        const size_t at = AL == kFlat ? (size_t)k : (size_t)row * p.K + k;
+        if constexpr (FMT == BEAM_MXFP8) {
+            const uint2 a = e4m3x8(half_of(v, 0)), b = e4m3x8(half_of(v, 1));
+            *reinterpret_cast<uint4 *>(p.codes + at) = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            *reinterpret_cast<uint2 *>(p.codes + at / 2) = make_uint2(e2m1x8(half_of(v, 0)), e2m1x8(half_of(v, 1)));
+        }
+        if (first) p.scales[AL == kFlat ? (size_t)j : p.map.at(row, j)] = (uint8_t)sb;
+    } else if (AL != kFlat && first && p.map.tiled && j < 4 * p.map.n4) {
+        p.scales[p.map.at(row, j)] = 0;
     }
 }
 
-template <typename T, int FMT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps) mx_quantize_kernel(const QuantArgs p)
+template <typename T, int FMT, int AL>
+__global__ void __launch_bounds__(kThreadsQ) mx_quantize_kernel(const QuantArgs p)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
     const float g = FMT == BEAM_NVFP4 ? *p.tensor_scale : 1.0f;
+    const float r6 = 1.0f / (6.0f * g);
     const T *x = static_cast<const T *>(p.x);
-    const long long step = (long long)gridDim.x * kWarps;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < p.units; u += step) {
-        const long long row = p.units_row == p.units ? 0 : u / p.units_row;
-        const long long k = (u - row * p.units_row) * kUnit + lane * 8;
-        const bool live = row < p.rows && k < p.K;
-        Raw8<T> raw = {};
-        if (live) raw = load_raw8<ALIGNED>(x + row * p.ldx + k);
-        quantize_unit<T, FMT>(p, raw, row, k, live, lane, g);
+    const int step = (int)gridDim.x * kThreadsQ, total = p.chunks.total;
+    // whole warps stay together: lanes past the end have nothing live
+    const int lane = threadIdx.x & 31;
+    for (int c0 = (int)blockIdx.x * kThreadsQ + (int)threadIdx.x; c0 - lane < total; c0 += kAhead * step) {
+        Raw16<T> raw[kAhead];
+        long long row[kAhead], k[kAhead];
+        bool live[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = total - 1 - (c0 + i * step);
+            raw[i] = Raw16<T>{};
+            if (c >= 0) {
+                int r, in_row;
+                p.chunks.at<AL>(c, r, in_row);
+                row[i] = p.row0 + r;
+                k[i] = (long long)in_row * kChunk;
+                live[i] = AL == kFlat || (row[i] < p.rows && k[i] < p.K);
+                if (live[i]) raw[i] = load_raw16<AL>(x + (AL == kFlat ? 0 : row[i] * p.ldx) + k[i]);
+            } else {   // nothing to write: past the end of the last tile's scales
+                row[i] = 0, k[i] = (long long)4 * p.map.n4 * block_size(FMT) + 16, live[i] = false;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (c0 - lane + i * step < total)
+                quantize_chunk<T, FMT, AL>(p, raw[i], row[i], k[i], live[i], g, r6);
     }
 }
 
@@ -122,40 +319,59 @@ __device__ __forceinline__ float tensor_scale_of(uint32_t amax_bits)
     return __uint_as_float((uint32_t)e << 23);
 }
 
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps) mx_amax_kernel(const QuantArgs p, float *out)
+template <typename T, int AL>
+__global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, float *out)
 {
+    constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
     const T *x = static_cast<const T *>(p.x);
-    const long long step = (long long)gridDim.x * kWarps;
+    const int step = (int)gridDim.x * kThreadsQ, total = p.chunks.total;
     uint32_t m = 0;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < p.units; u += step) {
-        const long long row = p.units_row == p.units ? 0 : u / p.units_row;
-        const long long k = (u - row * p.units_row) * kUnit + lane * 8;
-        const T *at = x + row * p.ldx + k;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (k + 8 <= p.K) {
-            unpack8(load_raw8<ALIGNED>(at), v);
-        } else {
+    for (int c0 = (int)blockIdx.x * kThreadsQ + (int)threadIdx.x; c0 < total; c0 += AHEAD * step) {
+        Raw16<T> raw[AHEAD];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < p.K) v[i] = to_f32(at[i]);
+        for (int i = 0; i < AHEAD; ++i) {
+            raw[i] = Raw16<T>{};
+            const int c = c0 + i * step;
+            if (c < total) {
+                int row, in_row;
+                p.chunks.at<AL>(c, row, in_row);
+                const long long k = (long long)in_row * kChunk;
+                const T *at = x + (AL == kFlat ? 0 : (p.row0 + row) * p.ldx) + k;
+                if (k + kChunk <= p.K) {
+                    raw[i] = load_raw16<AL>(at);
+                } else {
+                    for (int e = 0; k + e < p.K; ++e) {
+                        const uint32_t b = __float_as_uint(to_f32(at[e])) & 0x7fffffffu;
+                        m = max(m, b >= kInfBits ? 0u : b);
+                    }
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-            m = max(m, b >= kInfBits ? 0u : b);
+        for (int i = 0; i < AHEAD; ++i) {
+            const uint32_t b = amax_bits16(raw[i]);
+            if (b < kInfBits) {
+                m = max(m, b);
+            } else {   // the finite ones among infinities and NaN
+                float v[16];
+                unpack16(raw[i], v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t f = __float_as_uint(v[e]) & 0x7fffffffu;
+                    m = max(m, f >= kInfBits ? 0u : f);
+                }
+            }
         }
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    __shared__ uint32_t part[kWarps];
-    if (lane == 0) part[threadIdx.x >> 5] = m;
+    __shared__ uint32_t part[kThreadsQ / 32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) m = max(m, part[i]);
+        for (int i = 1; i < kThreadsQ / 32; ++i) m = max(m, part[i]);
         atomicMax(reinterpret_cast<int *>(out), __float_as_int(tensor_scale_of(m)));
     }
 }
@@ -164,57 +380,81 @@ struct DequantArgs {
     const uint8_t *codes, *scales;
     const float *tensor_scale;
     void *out;
-    long long rows, ldo, K, units, units_row;
+    long long ldo, K, row0;
+    Chunks chunks;
     ScaleMap map;
 };
 
-template <typename T, int FMT, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kWarps) mx_dequantize_kernel(const DequantArgs p)
+template <typename T, int FMT, int AL>
+__global__ void __launch_bounds__(kThreadsQ) mx_dequantize_kernel(const DequantArgs p)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
     const float g = p.tensor_scale ? *p.tensor_scale : 1.0f;
-    const long long step = (long long)gridDim.x * kWarps;
-    constexpr int BLOCK = FMT == BEAM_NVFP4 ? 16 : 32;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < p.units; u += step) {
-        const long long row = p.units_row == p.units ? 0 : u / p.units_row;
-        const long long k = (u - row * p.units_row) * kUnit + lane * 8;
-        if (k >= p.K) continue;
-        const size_t at = (size_t)row * p.K + k;
-        const uint32_t sb = p.scales[p.map.at(row, k / BLOCK)];
-        const float s = FMT == BEAM_NVFP4 ? e4m3x2_values(sb).x : ue8m0_value(sb);
-        float v[8];
-        if constexpr (FMT == BEAM_MXFP8) {
-            const uint2 c = *reinterpret_cast<const uint2 *>(p.codes + at);
+    const int step = (int)gridDim.x * kThreadsQ, total = p.chunks.total;
+    for (int c0 = (int)blockIdx.x * kThreadsQ + (int)threadIdx.x; c0 < total; c0 += kAhead * step) {
+        uint4 codes[kAhead];
+        uint32_t sb[kAhead];
+        long long row[kAhead], k[kAhead];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = e4m3x2_values((i < 2 ? c.x : c.y) >> (16 * (i & 1)) & 0xffffu);
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
-            }
-        } else {
-            const uint32_t c = *reinterpret_cast<const uint32_t *>(p.codes + at / 2);
-            uint32_t h[4];
-            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-                "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-                : "r"(c));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + i * step;
+            codes[i] = make_uint4(0u, 0u, 0u, 0u), sb[i] = 0u, row[i] = 0, k[i] = 0;
+            if (c < total) {
+                int r, in_row;
+                p.chunks.at<AL>(c, r, in_row);
+                row[i] = p.row0 + r;
+                k[i] = (long long)in_row * kChunk;
+                const size_t at = AL == kFlat ? (size_t)k[i] : (size_t)row[i] * p.K + k[i];
+                if constexpr (FMT == BEAM_MXFP8) {
+                    codes[i] = *reinterpret_cast<const uint4 *>(p.codes + at);
+                } else {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(p.codes + at / 2);
+                    codes[i].x = q.x, codes[i].y = q.y;
+                }
+                const long long j = k[i] / block_size(FMT);
+                sb[i] = p.scales[AL == kFlat ? (size_t)j : p.map.at(row[i], j)];
             }
         }
-        // element * block scale first: exact in FP32 (it may only leave the
-        // normal range for power-of-two scales next to 2^-127), then the
-        // tensor scale, rounded once
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * s * g;
-        store8<ALIGNED>(static_cast<T *>(p.out) + row * p.ldo + k, v);
+        for (int i = 0; i < kAhead; ++i) {
+            if (c0 + i * step >= total) break;
+            const float s = FMT == BEAM_NVFP4 ? e4m3x2_values(sb[i]).x : ue8m0_value(sb[i]);
+            float v[16];
+            if constexpr (FMT == BEAM_MXFP8) {
+                const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = e4m3x2_values(w[e / 2] >> (16 * (e & 1)) & 0xffffu);
+                    v[2 * e] = f.x, v[2 * e + 1] = f.y;
+                }
+            } else {
+                const uint32_t w[2] = {codes[i].x, codes[i].y};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t h[4];
+                    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+                        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+                        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                        : "r"(w[q]));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+                        v[8 * q + 2 * e] = f.x, v[8 * q + 2 * e + 1] = f.y;
+                    }
+                }
+            }
+            // element * block scale first: exact in FP32 (it may only leave the
+            // normal range for power-of-two scales next to 2^-127), then the
+            // tensor scale, rounded once
+            scale16(v, s);
+            if (p.tensor_scale) scale16(v, g);
+            store16<AL>(static_cast<T *>(p.out) + (AL == kFlat ? 0 : row[i] * p.ldo) + k[i], v);
+        }
     }
 }
 
@@ -237,36 +477,79 @@ __global__ void mx_tile_scales_kernel(const uint8_t *scales, uint8_t *tiled, lon
     }
 }
 
-// Blocks for `units` warp units: every SM's 8 resident blocks at most.
-int grid_for(long long units)
+// Blocks for `n` threads' work, at most `per_sm` an SM: 8, or 16 where the
+// stores are most of the traffic (reading back 20480 x 5120 NVFP4: 44 us, 50 with 8).
+int grid_for(long long n, int per_sm = 8)
 {
-    const long long need = (units + kWarps - 1) / kWarps;
-    const long long most = (long long)sm_count() * 8;
+    const long long need = (n + kThreadsQ - 1) / kThreadsQ;
+    const long long most = (long long)sm_count() * per_sm;
     return (int)(need < most ? need : most);
 }
 
-template <int FMT>
-cudaError_t launch_quantize(const QuantArgs &a, int dtype, bool al, cudaStream_t s)
+// How the chunks of a matrix lie.
+int chunk_alignment(const void *p, bool flat, long long ld, int dtype)
 {
-    const dim3 grid(grid_for(a.units)), block(32 * kWarps);
-#define BEAM_Q(T) (al ? launch_pdl(mx_quantize_kernel<T, FMT, true>, grid, block, 0, s, a) \
-                      : launch_pdl(mx_quantize_kernel<T, FMT, false>, grid, block, 0, s, a))
-    if (dtype == BEAM_BF16) return BEAM_Q(__nv_bfloat16);
-    if (dtype == BEAM_F16) return BEAM_Q(__half);
-    return BEAM_Q(float);
-#undef BEAM_Q
+    if (flat && aligned(p, 32)) return kFlat;
+    const long long pitch = (flat ? 32 : ld) * dtype_size(dtype);
+    return aligned(p, 32) && pitch % 32 == 0 ? 32 : aligned(p, 16) && pitch % 16 == 0 ? 16 : 0;
+}
+
+#define BEAM_ALIGNED(kernel, T, ...)                                    \
+    (al == kFlat ? launch_pdl(kernel<T, ##__VA_ARGS__, kFlat>, grid, dim3(kThreadsQ), 0, s, BEAM_ARGS) \
+     : al == 32 ? launch_pdl(kernel<T, ##__VA_ARGS__, 32>, grid, dim3(kThreadsQ), 0, s, BEAM_ARGS) \
+     : al == 16 ? launch_pdl(kernel<T, ##__VA_ARGS__, 16>, grid, dim3(kThreadsQ), 0, s, BEAM_ARGS) \
+                : launch_pdl(kernel<T, ##__VA_ARGS__, 0>, grid, dim3(kThreadsQ), 0, s, BEAM_ARGS))
+#define BEAM_TYPED(kernel, ...)                                         \
+    (dtype == BEAM_BF16 ? BEAM_ALIGNED(kernel, __nv_bfloat16, ##__VA_ARGS__) \
+     : dtype == BEAM_F16 ? BEAM_ALIGNED(kernel, __half, ##__VA_ARGS__)  \
+                         : BEAM_ALIGNED(kernel, float, ##__VA_ARGS__))
+
+template <int FMT>
+cudaError_t launch_quantize(const QuantArgs &a, int dtype, int al, cudaStream_t s)
+{
+    const dim3 grid(grid_for(a.chunks.total));
+#define BEAM_ARGS a
+    return BEAM_TYPED(mx_quantize_kernel, FMT);
+#undef BEAM_ARGS
 }
 
 template <int FMT>
-cudaError_t launch_dequantize(const DequantArgs &a, int dtype, bool al, cudaStream_t s)
+cudaError_t launch_dequantize(const DequantArgs &a, int dtype, int al, cudaStream_t s)
 {
-    const dim3 grid(grid_for(a.units)), block(32 * kWarps);
-#define BEAM_D(T) (al ? launch_pdl(mx_dequantize_kernel<T, FMT, true>, grid, block, 0, s, a) \
-                      : launch_pdl(mx_dequantize_kernel<T, FMT, false>, grid, block, 0, s, a))
-    if (dtype == BEAM_BF16) return BEAM_D(__nv_bfloat16);
-    if (dtype == BEAM_F16) return BEAM_D(__half);
-    return BEAM_D(float);
-#undef BEAM_D
+    const dim3 grid(grid_for(a.chunks.total, 16));
+#define BEAM_ARGS a
+    return BEAM_TYPED(mx_dequantize_kernel, FMT);
+#undef BEAM_ARGS
+}
+
+cudaError_t launch_amax(const QuantArgs &a, int dtype, int al, float *out, cudaStream_t s)
+{
+    const dim3 grid(a.chunks.total ? grid_for(a.chunks.total) : 1);
+#define BEAM_ARGS a, out
+    return BEAM_TYPED(mx_amax_kernel);
+#undef BEAM_ARGS
+}
+
+// launch(a) over slices of rows of `per` chunks each (rows == 1: over chunks;
+// `step` advances a's pointers by that many then).
+template <typename Args, typename Step, typename Launch>
+cudaError_t in_slices(Args a, long long rows, long long per, Step step, Launch launch)
+{
+    if (rows == 1) {
+        for (long long done = 0; done < per; done += kSlice) {
+            Args part = a;
+            step(part, done);
+            part.chunks = Chunks(1, (int)(per - done < kSlice ? per - done : kSlice));
+            if (cudaError_t e = launch(part)) return e;
+        }
+        return cudaSuccess;
+    }
+    const long long most = per < kSlice ? kSlice / per : 1;
+    for (a.row0 = 0; a.row0 < rows; a.row0 += most) {
+        a.chunks = Chunks((int)(rows - a.row0 < most ? rows - a.row0 : most), (int)per);
+        if (cudaError_t e = launch(a)) return e;
+    }
+    return cudaSuccess;
 }
 
 int check_shape(int format, long long rows, int K, int layout)
@@ -307,18 +590,15 @@ int beam_mx_tensor_scale(void *stream, const void *x, int dtype, long long rows,
     if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
     if (int rc = check_cuda(cudaMemsetAsync(tensor_scale, 0, sizeof(float), s), "cudaMemsetAsync")) return rc;
     const bool flat = rows == 1 || ldx == K;
-    const long long n = flat ? rows * (long long)K : K;
-    const bool al = rows_aligned16(x, flat ? 8 : ldx, dtype);
-    const long long per = (n + kUnit - 1) / kUnit;
-    const QuantArgs a{x, nullptr, nullptr, nullptr, flat ? 1 : rows, ldx, n, flat ? per : per * rows, per, ScaleMap(0, 1)};
-    const dim3 grid(a.units ? grid_for(a.units) : 1), block(32 * kWarps);
-    cudaError_t e;
-#define BEAM_A(T) (al ? launch_pdl(mx_amax_kernel<T, true>, grid, block, 0, s, a, tensor_scale) \
-                      : launch_pdl(mx_amax_kernel<T, false>, grid, block, 0, s, a, tensor_scale))
-    if (dtype == BEAM_BF16) e = BEAM_A(__nv_bfloat16);
-    else if (dtype == BEAM_F16) e = BEAM_A(__half);
-    else e = BEAM_A(float);
-#undef BEAM_A
+    QuantArgs a{x, nullptr, nullptr, nullptr, rows, ldx, K, 0, Chunks(0, 1), ScaleMap(0, 1)};
+    const int al = chunk_alignment(x, flat, ldx, dtype);
+    const auto launch = [&](const QuantArgs &part) { return launch_amax(part, dtype, al, tensor_scale, s); };
+    if (flat) a.rows = 1, a.K = rows * (long long)K;
+    if (a.K == 0) return check_cuda(launch(a), "beam_mx_tensor_scale");   // no rows
+    const cudaError_t e = in_slices(a, a.rows, (a.K + kChunk - 1) / kChunk, [&](QuantArgs &part, long long c) {
+        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
+        part.K -= c * kChunk;
+    }, launch);
     return check_cuda(e, "beam_mx_tensor_scale");
 }
 
@@ -339,23 +619,25 @@ int beam_mx_quantize(void *stream, const void *x, int dtype, long long rows, int
     if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
     const int n = K / block_of(format);
     const bool flat = layout == BEAM_SCALES_ROWS && (rows == 1 || ldx == K);
-    QuantArgs a{x, tensor_scale, codes, scales, rows, ldx, K, 0, 0, ScaleMap(layout, n)};
-    if (flat) {
-        a.rows = 1;
-        a.K = rows * (long long)K;
-        a.units = a.units_row = (a.K + kUnit - 1) / kUnit;
-    } else {
-        // tiled: the unit range covers the padding rows and scales too
-        const long long span = layout == BEAM_SCALES_TILED ? (long long)a.map.n4 * 4 * block_of(format) : K;
-        a.units_row = (span + kUnit - 1) / kUnit;
-        a.units = a.units_row * (layout == BEAM_SCALES_TILED ? (rows + 127) / 128 * 128 : rows);
-    }
-    const bool al = rows_aligned16(x, flat ? 8 : ldx, dtype);
+    QuantArgs a{x, tensor_scale, codes, scales, rows, ldx, K, 0, Chunks(), ScaleMap(layout, n)};
+    const int al = chunk_alignment(x, flat, ldx, dtype);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (format == BEAM_NVFP4) e = launch_quantize<BEAM_NVFP4>(a, dtype, al, s);
-    else if (format == BEAM_MXFP4) e = launch_quantize<BEAM_MXFP4>(a, dtype, al, s);
-    else e = launch_quantize<BEAM_MXFP8>(a, dtype, al, s);
+    const auto launch = [&](const QuantArgs &part) {
+        return format == BEAM_NVFP4   ? launch_quantize<BEAM_NVFP4>(part, dtype, al, s)
+               : format == BEAM_MXFP4 ? launch_quantize<BEAM_MXFP4>(part, dtype, al, s)
+                                      : launch_quantize<BEAM_MXFP8>(part, dtype, al, s);
+    };
+    // tiled: the chunks cover the tiles' padding rows and scales too
+    const bool tiled = layout == BEAM_SCALES_TILED;
+    if (flat) a.rows = 1, a.K = rows * (long long)K;
+    const long long all = flat ? 1 : tiled ? (rows + 127) / 128 * 128 : rows;
+    const long long per = tiled ? (long long)a.map.n4 * 4 * block_of(format) / kChunk : a.K / kChunk;
+    const cudaError_t e = in_slices(a, all, per, [&](QuantArgs &part, long long c) {
+        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
+        part.codes = codes + (format == BEAM_MXFP8 ? c * kChunk : c * kChunk / 2);
+        part.scales = scales + c * kChunk / block_of(format);
+        part.K -= c * kChunk;
+    }, launch);
     return check_cuda(e, "beam_mx_quantize");
 }
 
@@ -374,16 +656,21 @@ int beam_mx_dequantize(void *stream, const uint8_t *codes, const uint8_t *scales
         return fail(BEAM_ERR_INVALID_ARG, "a pointer is not aligned");
     if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
     const bool flat = layout == BEAM_SCALES_ROWS && (rows == 1 || ldo == K);
-    DequantArgs a{codes, scales, tensor_scale, out, rows, ldo, K, 0, 0, ScaleMap(layout, K / block_of(format))};
-    if (flat) a.rows = 1, a.K = rows * (long long)K;
-    a.units_row = (a.K + kUnit - 1) / kUnit;
-    a.units = a.units_row * a.rows;
-    const bool al = rows_aligned16(out, flat ? 8 : ldo, dtype);
+    DequantArgs a{codes, scales, tensor_scale, out, ldo, K, 0, Chunks(), ScaleMap(layout, K / block_of(format))};
+    const int al = chunk_alignment(out, flat, ldo, dtype);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (format == BEAM_NVFP4) e = launch_dequantize<BEAM_NVFP4>(a, dtype, al, s);
-    else if (format == BEAM_MXFP4) e = launch_dequantize<BEAM_MXFP4>(a, dtype, al, s);
-    else e = launch_dequantize<BEAM_MXFP8>(a, dtype, al, s);
+    const auto launch = [&](const DequantArgs &part) {
+        return format == BEAM_NVFP4   ? launch_dequantize<BEAM_NVFP4>(part, dtype, al, s)
+               : format == BEAM_MXFP4 ? launch_dequantize<BEAM_MXFP4>(part, dtype, al, s)
+                                      : launch_dequantize<BEAM_MXFP8>(part, dtype, al, s);
+    };
+    if (flat) a.K = rows * (long long)K;
+    const cudaError_t e = in_slices(a, flat ? 1 : rows, a.K / kChunk, [&](DequantArgs &part, long long c) {
+        part.codes = codes + (format == BEAM_MXFP8 ? c * kChunk : c * kChunk / 2);
+        part.scales = scales + c * kChunk / block_of(format);
+        part.out = static_cast<uint8_t *>(out) + c * kChunk * dtype_size(dtype);
+        part.K -= c * kChunk;
+    }, launch);
     return check_cuda(e, "beam_mx_dequantize");
 }
 
@@ -398,7 +685,7 @@ int beam_mx_tile_scales(void *stream, int format, const uint8_t *scales, long lo
     if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
     const ScaleMap map(BEAM_SCALES_TILED, K / block_of(format));
     const long long groups = (rows + 127) / 128 * 128 * map.n4;
-    return check_cuda(launch_pdl(mx_tile_scales_kernel, dim3(grid_for(groups / 32 + 1)), dim3(256), 0,
+    return check_cuda(launch_pdl(mx_tile_scales_kernel, dim3(grid_for(groups)), dim3(256), 0,
                                  static_cast<cudaStream_t>(stream), scales, tiled, rows, map, groups),
                       "beam_mx_tile_scales");
 }

@@ -18,6 +18,7 @@ int check_cuda(cudaError_t e, const char *what);
 inline bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int dtype_size(int dtype) { return dtype == BEAM_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype >= BEAM_BF16 && dtype <= BEAM_F32; }
+constexpr int block_size(int format) { return format == BEAM_NVFP4 ? 16 : 32; }
 inline int block_of(int format) { return format == BEAM_NVFP4 ? 16 : 32; }
 inline bool format_ok(int format) { return format >= BEAM_NVFP4 && format <= BEAM_MXFP8; }
 inline bool layout_ok(int layout) { return layout == BEAM_SCALES_ROWS || layout == BEAM_SCALES_TILED; }

@@ -25,28 +25,133 @@ struct NormArgs {
     ScaleMap map;
 };
 
-// Store V (8 or 1) consecutive output elements in the output's type.
-template <int V>
-__device__ __forceinline__ void store_out(void *out, int dtype, size_t at, const float (&y)[V])
+// --- eight elements at any address ------------------------------------------------
+//
+// Rows of an odd length, or of a strided view, start anywhere.  Their vectors
+// of 8 elements are read as the aligned 16-byte units that hold them and
+// shifted into place (all vectors of a row by the same `o` bytes), and
+// written the same way, with the part that lies in a lane's first unit taken
+// from the lane below.  1000 x 2563 fp16: SHIFTED us; 10.0 us with 2-byte accesses.
+
+template <typename T> struct Units { uint32_t w[2 * sizeof(T) + 4]; };
+
+// Elements e .. e + 7 of a row of n elements that starts at `row`.  [lo, hi)
+// is the tensor: units that reach out of it, and elements past the row's
+// end, are not read.  o: bytes to shift by.
+template <typename T>
+__device__ __forceinline__ Units<T> load_units(const T *row, int e, int n, const void *lo, const void *hi, uint32_t &o)
 {
-    if constexpr (V == 8) {
-        if (dtype == BEAM_BF16) store8<true>(static_cast<__nv_bfloat16 *>(out) + at, y);
-        else if (dtype == BEAM_F16) store8<true>(static_cast<__half *>(out) + at, y);
-        else store8<true>(static_cast<float *>(out) + at, y);
+    constexpr int NU = sizeof(T) / 2;
+    Units<T> u = {};
+    const T *p = row + e;
+    o = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - o);
+    const int units = o ? NU + 1 : NU;
+    if (e + 8 <= n && static_cast<const void *>(q) >= lo && static_cast<const void *>(q + units) <= hi) {
+#pragma unroll
+        for (int i = 0; i <= NU; ++i)
+            if (i < units) {
+                const uint4 v = q[i];
+                u.w[4 * i] = v.x, u.w[4 * i + 1] = v.y, u.w[4 * i + 2] = v.z, u.w[4 * i + 3] = v.w;
+            }
     } else {
-        if (dtype == BEAM_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(y[0]);
-        else if (dtype == BEAM_F16) static_cast<__half *>(out)[at] = __float2half_rn(y[0]);
-        else static_cast<float *>(out)[at] = y[0];
+        o = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < n) {
+                if constexpr (sizeof(T) == 4) u.w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+                else u.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << (16 * (i & 1));
+            }
+    }
+    return u;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> shift_units(const Units<T> &u, uint32_t o)
+{
+    constexpr int N = 2 * sizeof(T);
+    uint32_t w[N + 4];
+#pragma unroll
+    for (int i = 0; i < N + 4; ++i) w[i] = u.w[i];
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) w[i] = o & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) w[i] = o & 4u ? w[i + 1] : w[i];
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = sizeof(T) == 2 && (o & 2u) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    return r;
+}
+
+// v to elements e .. e + 7 of the row (those below n).  Whole warps call it,
+// lane l + 1 with the vector behind lane l's where both have one.
+template <typename T>
+__device__ __forceinline__ void store_any8(T *row, int e, int n, const float (&v)[8])
+{
+    constexpr int N = 2 * sizeof(T);
+    T *p = row + e;
+    const uint32_t o = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const int lane = threadIdx.x & 31;
+    const bool whole = e + 8 <= n;
+    const uint32_t wholes = __ballot_sync(0xffffffffu, whole);
+    uint32_t c[N + 4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (sizeof(T) == 4) c[i + 4] = __float_as_uint(v[i]);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value) c[i + 4] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        else c[i + 4] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __shfl_up_sync(0xffffffffu, c[N + i], 1);
+    if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < n) p[i] = from_f32<T>(v[i]);
+        return;
+    }
+    // bytes 16 - o and on of (the lane below's last 16 bytes, this lane's)
+    const uint32_t s = 16u - o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = s & 16u ? c[i + 4] : c[i];
+    const bool below = lane > 0 && ((wholes >> (lane - 1)) & 1u);
+    const bool above = lane < 31 && ((wholes >> (lane + 1)) & 1u);
+    if (o) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) c[i] = s & 8u ? c[i + 2] : c[i];
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) c[i] = s & 4u ? c[i + 1] : c[i];
+        if constexpr (sizeof(T) == 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = s & 2u ? __funnelshift_r(c[i], c[i + 1], 16) : c[i];
+    }
+    uint4 *q = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(p) - o);
+    if (!o || below) q[0] = make_uint4(c[0], c[1], c[2], c[3]);
+    if constexpr (sizeof(T) == 4) q[1] = make_uint4(c[4], c[5], c[6], c[7]);
+    if (o) {
+        // the ends of a run of lanes, element by element
+        const int first = (int)(s / sizeof(T));   // elements of this lane in its first unit
+        const int last = 8 - (int)(o / sizeof(T));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((!below && i < first) || (!above && i >= last)) p[i] = from_f32<T>(v[i]);
     }
 }
 
+// --- the kernel -------------------------------------------------------------------
+
+struct Bounds {
+    const void *x_end, *r_end;   // one past the last element of x and residual
+};
+
 // A row per block (WARP_ROWS = 0) or per warp.  Thread t of the row's `nt`
-// holds the V-element vectors t, t + nt, ...: NV of them at most.
-//   V = 8   16-byte aligned rows, H a multiple of 8; a 32-element MXFP8 block
-//           is four neighbouring lanes;
-//   V = 1   everything else; a block is one warp-wide step.
-template <typename XT, typename RT, bool HAS_R, int V, int NV, bool WARP_ROWS>
-__global__ void __launch_bounds__(WARP_ROWS ? 128 : V == 8 && NV == 2 ? 512 : 1024) rms_norm_kernel(const NormArgs p)
+// holds the 8-element vectors t, t + nt, ...: NV of them at most.  ALIGNED:
+// every row of every matrix starts on 16 bytes and H is a multiple of 8.  A
+// 32-element MXFP8 block is four neighbouring lanes.  EARLY: gamma is read
+// before the row's sum is known, which shortens a row's chain of waits (64 x
+// 5120: 2.7 us, 3.3 without) but takes registers that many rows need more as
+// rows in flight (8192 x 5120, no residual: 46 us, 32 without).
+template <typename XT, typename RT, bool HAS_R, bool ALIGNED, int NV, bool WARP_ROWS, bool EARLY>
+__global__ void __launch_bounds__(WARP_ROWS ? 128 : NV == 2 ? 512 : 1024) rms_norm_kernel(const NormArgs p, const Bounds end)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -61,55 +166,84 @@ __global__ void __launch_bounds__(WARP_ROWS ? 128 : V == 8 && NV == 2 ? 512 : 10
                 *reinterpret_cast<uint32_t *>(p.scales + p.map.at(row, 4 * j)) = 0;
         return;
     }
-    const int nvec = p.H / V;   // V = 8 only with H a multiple of 8
-    float s[NV][V];
+    float s[NV][8];
     float sum = 0.f;
     const XT *x = static_cast<const XT *>(p.x) + (size_t)row * p.ldx;
     const RT *r = HAS_R ? static_cast<const RT *>(p.r) + (size_t)row * p.ldr : nullptr;
     RT *ro = HAS_R ? static_cast<RT *>(p.ro) + (size_t)row * p.ldro : nullptr;
-    if constexpr (V == 8) {
+    float g[EARLY ? NV : 1][8];
+    const auto load_gamma = [&](int e, float (&v)[8]) {
+        if constexpr (ALIGNED) {
+            const float4 a = *reinterpret_cast<const float4 *>(p.gamma + e), b = *reinterpret_cast<const float4 *>(p.gamma + e + 4);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            uint32_t o;
+            const Units<float> u = load_units(p.gamma, e, p.H, p.gamma, p.gamma + p.H, o);
+            unpack8(shift_units(u, o), v);
+        }
+    };
+    if constexpr (ALIGNED) {
         Raw8<XT> xr[NV];
         Raw8<RT> rr[HAS_R ? NV : 1];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (t + i * nt < nvec) {
-                xr[i] = load_raw8<true>(x + (size_t)(t + i * nt) * 8);
-                if constexpr (HAS_R) rr[i] = load_raw8<true>(r + (size_t)(t + i * nt) * 8);
+        for (int i = 0; i < NV; ++i) {
+            const int e = (t + i * nt) * 8;
+            if (e < p.H) {
+                xr[i] = load_raw8<true>(x + e);
+                if constexpr (HAS_R) rr[i] = load_raw8<true>(r + e);
             }
+        }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (t + i * nt < nvec) {
-                float xv[8];
-                unpack8(xr[i], xv);
+        for (int i = 0; EARLY && i < NV; ++i) {
+            const int e = (t + i * nt) * 8;
+            if (e < p.H) load_gamma(e, g[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = (t + i * nt) * 8;
+            if (e < p.H) {
+                unpack8(xr[i], s[i]);
                 if constexpr (HAS_R) {
                     float rv[8];
                     unpack8(rr[i], rv);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) s[i][q] = fmaf(p.alpha, rv[q], p.beta * xv[q]);
-                    store8<true>(ro + (size_t)(t + i * nt) * 8, s[i]);
+                    for (int q = 0; q < 8; ++q) s[i][q] = fmaf(p.alpha, rv[q], p.beta * s[i][q]);
+                    store8<true>(ro + e, s[i]);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) s[i][q] = p.beta * xv[q];
+                    for (int q = 0; q < 8; ++q) s[i][q] *= p.beta;
                 }
 #pragma unroll
                 for (int q = 0; q < 8; ++q) sum = fmaf(s[i][q], s[i][q], sum);
             }
+        }
     } else {
+        Units<XT> xu[NV];
+        Units<RT> ru[HAS_R ? NV : 1];
+        uint32_t xo[NV], rs[HAS_R ? NV : 1];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = t + i * nt;
-            s[i][0] = 0.f;
-            if (e < nvec) {
-                s[i][0] = p.beta * to_f32(x[e]);
-                if constexpr (HAS_R) s[i][0] = fmaf(p.alpha, to_f32(r[e]), s[i][0]);
-            }
+            const int e = (t + i * nt) * 8;
+            xu[i] = load_units(x, e, p.H, p.x, end.x_end, xo[i]);
+            if constexpr (HAS_R) ru[i] = load_units(r, e, p.H, p.r, end.r_end, rs[i]);
         }
 #pragma unroll
+        for (int i = 0; EARLY && i < NV; ++i) load_gamma((t + i * nt) * 8, g[i]);
+#pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = t + i * nt;
-            if constexpr (HAS_R)
-                if (e < nvec) ro[e] = from_f32<RT>(s[i][0]);
-            sum = fmaf(s[i][0], s[i][0], sum);
+            unpack8(shift_units(xu[i], xo[i]), s[i]);   // zeros past the row's end
+            if constexpr (HAS_R) {
+                float rv[8];
+                unpack8(shift_units(ru[i], rs[i]), rv);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s[i][q] = fmaf(p.alpha, rv[q], p.beta * s[i][q]);
+                store_any8(ro, (t + i * nt) * 8, p.H, s[i]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s[i][q] *= p.beta;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sum = fmaf(s[i][q], s[i][q], sum);
         }
     }
 #pragma unroll
@@ -126,49 +260,44 @@ __global__ void __launch_bounds__(WARP_ROWS ? 128 : V == 8 && NV == 2 ? 512 : 10
     const float scale = 1.0f / sqrtf(sum / (float)p.H + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int vec = t + i * nt;
         // an MXFP8 block's lanes are all in or all out of the row (H a
         // multiple of 32 then), so its shuffles run on whole groups
-        if constexpr (V == 8) {
-            float y[8];
-            uint32_t m = 0;
-            if (vec < nvec) {
-                const float4 g0 = reinterpret_cast<const float4 *>(p.gamma)[2 * vec];
-                const float4 g1 = reinterpret_cast<const float4 *>(p.gamma)[2 * vec + 1];
-                const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+        const int e = (t + i * nt) * 8;
+        const bool in = e < p.H;
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        uint32_t m = 0;
+        if (in) {
+            float gl[8];
+            if constexpr (!EARLY) load_gamma(e, gl);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = s[i][q] * scale * g[q];
-                if (p.out) store_out<8>(p.out, p.out_dtype, (size_t)row * p.ldo + (size_t)vec * 8, y);
-                m = amax_bits8(y);
-            }
-            if (p.codes) {
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                if (vec < nvec) {
-                    const bool bad = m >= kInfBits;
-                    const uint32_t b = ue8m0_byte<kTop448>(__uint_as_float(m));
-                    const float inv = ue8m0_inverse(b);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] = bad ? 0.f : y[q] * inv;
-                    *reinterpret_cast<uint2 *>(p.codes + (size_t)row * p.H + (size_t)vec * 8) = e4m3x8(y);
-                    if ((lane & 3) == 0) p.scales[p.map.at(row, vec >> 2)] = bad ? 0xff : (uint8_t)b;
-                }
-            }
-        } else {
-            const bool in = vec < nvec;
-            float y[1] = {in ? s[i][0] * scale * p.gamma[vec] : 0.f};
-            if (in && p.out) store_out<1>(p.out, p.out_dtype, (size_t)row * p.ldo + vec, y);
-            if (p.codes) {
-                const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(y[0]) & 0x7fffffffu);
+            for (int q = 0; q < 8; ++q) y[q] = s[i][q] * scale * (EARLY ? g[EARLY ? i : 0][q] : gl[q]);
+            m = amax_bits8(y);
+        }
+        if (p.out) {
+            const size_t at = (size_t)row * p.ldo;
+            if constexpr (ALIGNED) {
                 if (in) {
-                    const bool bad = m >= kInfBits;
-                    const uint32_t b = ue8m0_byte<kTop448>(__uint_as_float(m));
-                    const float v = bad ? 0.f : y[0] * ue8m0_inverse(b);
-                    uint16_t d;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.0f), "f"(v));
-                    p.codes[(size_t)row * p.H + vec] = (uint8_t)d;
-                    if (lane == 0) p.scales[p.map.at(row, vec >> 5)] = bad ? 0xff : (uint8_t)b;
+                    if (p.out_dtype == BEAM_BF16) store8<true>(static_cast<__nv_bfloat16 *>(p.out) + at + e, y);
+                    else if (p.out_dtype == BEAM_F16) store8<true>(static_cast<__half *>(p.out) + at + e, y);
+                    else store8<true>(static_cast<float *>(p.out) + at + e, y);
                 }
+            } else {
+                if (p.out_dtype == BEAM_BF16) store_any8(static_cast<__nv_bfloat16 *>(p.out) + at, e, p.H, y);
+                else if (p.out_dtype == BEAM_F16) store_any8(static_cast<__half *>(p.out) + at, e, p.H, y);
+                else store_any8(static_cast<float *>(p.out) + at, e, p.H, y);
+            }
+        }
+        if (p.codes) {
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (in) {
+                const bool bad = m >= kInfBits;
+                const uint32_t b = ue8m0_byte<kTop448>(__uint_as_float(m));
+                const float inv = ue8m0_inverse(b);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = bad ? 0.f : y[q] * inv;
+                *reinterpret_cast<uint2 *>(p.codes + (size_t)row * p.H + e) = e4m3x8(y);
+                if ((lane & 3) == 0) p.scales[p.map.at(row, e >> 5)] = bad ? 0xff : (uint8_t)b;
             }
         }
     }
@@ -176,35 +305,39 @@ __global__ void __launch_bounds__(WARP_ROWS ? 128 : V == 8 && NV == 2 ? 512 : 10
     if (p.codes && p.map.tiled && t < 4 * p.map.n4 - p.map.n) p.scales[p.map.at(row, p.map.n + t)] = 0;
 }
 
-template <typename XT, typename RT, bool HAS_R>
-cudaError_t launch(const NormArgs &a, bool vec, cudaStream_t stream)
+template <typename XT, typename RT, bool HAS_R, bool ALIGNED>
+cudaError_t launch(const NormArgs &a, const Bounds &end, cudaStream_t stream)
 {
     const int rows = a.codes && a.map.tiled ? (a.T + 127) / 128 * 128 : a.T;
-    if (vec) {
-        const int nvec = a.H / 8;
-        if (nvec <= 32 * 4) {
-            const dim3 grid((rows + 3) / 4), block(128);
-            if (nvec <= 32) return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 8, 1, true>, grid, block, 0, stream, a);
-            return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 8, 4, true>, grid, block, 0, stream, a);
-        }
-        const int nv = nvec <= 1024 ? 2 : 4;
-        const dim3 block(((nvec + nv - 1) / nv + 31) / 32 * 32);
-        if (nv == 2) return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 8, 2, false>, dim3(rows), block, 0, stream, a);
-        return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 8, 4, false>, dim3(rows), block, 0, stream, a);
-    }
-    if (a.H <= 8 * 1024) {
-        const dim3 block(((a.H + 7) / 8 + 31) / 32 * 32);
-        return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 1, 8, false>, dim3(rows), block, 0, stream, a);
-    }
-    return launch_pdl(rms_norm_kernel<XT, RT, HAS_R, 1, 32, false>, dim3(rows), dim3(1024), 0, stream, a);
+    const int nvec = (a.H + 7) / 8;
+#define BEAM_NORM(NV, WARP, EARLY, grid, block) \
+    launch_pdl(rms_norm_kernel<XT, RT, HAS_R, ALIGNED, NV, WARP, EARLY>, dim3(grid), dim3(block), 0, stream, a, end)
+    if (nvec <= 32) return BEAM_NORM(1, true, true, (rows + 3) / 4, 128);
+    // unaligned rows of 1001: four vectors a lane take 156 registers (31 us for
+    // 8000 rows), a block of two vectors a thread WIDEQ
+    if (ALIGNED && nvec <= 32 * 4) return BEAM_NORM(4, true, false, (rows + 3) / 4, 128);
+    const int nv = nvec <= 1024 ? 2 : 4;
+    const int block = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    if (nv == 4) return BEAM_NORM(4, false, false, rows, block);
+    if (rows <= 16 * sm_count()) return BEAM_NORM(2, false, true, rows, block);
+    return BEAM_NORM(2, false, false, rows, block);
+#undef BEAM_NORM
+}
+
+template <typename XT, typename RT, bool HAS_R>
+cudaError_t launch_any(const NormArgs &a, bool vec, cudaStream_t stream)
+{
+    Bounds end{static_cast<const XT *>(a.x) + (size_t)(a.T - 1) * a.ldx + a.H,
+               HAS_R ? static_cast<const RT *>(a.r) + (size_t)(a.T - 1) * a.ldr + a.H : nullptr};
+    return vec ? launch<XT, RT, HAS_R, true>(a, end, stream) : launch<XT, RT, HAS_R, false>(a, end, stream);
 }
 
 template <typename XT, int XD>
 cudaError_t launch_x(const NormArgs &a, int residual_dtype, bool vec, cudaStream_t stream)
 {
-    if (!a.r) return launch<XT, XT, false>(a, vec, stream);
-    if (residual_dtype == XD) return launch<XT, XT, true>(a, vec, stream);
-    return launch<XT, float, true>(a, vec, stream);
+    if (!a.r) return launch_any<XT, XT, false>(a, vec, stream);
+    if (residual_dtype == XD) return launch_any<XT, XT, true>(a, vec, stream);
+    return launch_any<XT, float, true>(a, vec, stream);
 }
 
 }  // namespace

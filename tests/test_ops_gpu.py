@@ -632,3 +632,31 @@ def test_route_long_batch_strided_rows():
     some = ops.route_scores(l[8500:8600], 8, bias=bias, n_group=8, topk_group=4)
     assert torch.equal(some[0], want[0][8500:8600]) and torch.equal(some[1], want[1][8500:8600])
     check_route(l[:700], 8, "sigmoid", bias, 8, 4)
+
+
+@pytest.mark.parametrize("xt,rt", TYPES)
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 9), (3, 255), (5, 261), (4, 1031), (3, 2563), (2, 8191), (2, 9001)])
+def test_norm_writes_its_rows_alone(xt, rt, T, H):
+    """Rows at every offset from a vector's alignment, in and out: the bytes around them stay, and the residual may be
+    updated in place."""
+    gamma = (1 + 0.1 * torch.randn(H + 1, generator=torch.Generator().manual_seed(H))).cuda()[1:]
+    x0, r0 = rand(T, H, xt, H), None if rt is None else rand(T, H, rt, H + 1)
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        for off in (0, 1, 2, 3, 5, 7):
+            def room(t, like=None):
+                b = torch.full((T, H + 9), 7.0, dtype=t, device="cuda")
+                if like is not None:
+                    b[:, off:off + H] = like
+                return b
+
+            def kept(b):
+                return (b[:, :off] == 7.0).all() and (b[:, off + H:] == 7.0).all()
+            bx, bo = room(xt, x0), room(dtype)
+            br = None if rt is None else room(rt, r0)
+            r = None if rt is None else br[:, off:off + H]
+            want = ops.rms_norm(x0, gamma, residual=r0, alpha=0.9, beta=0.3, dtype=dtype)
+            ops.rms_norm(bx[:, off:off + H], gamma, residual=r, alpha=0.9, beta=0.3, dtype=dtype, out=bo[:, off:off + H],
+                         residual_out=r)
+            assert torch.equal(bo[:, off:off + H], want.out) and kept(bo) and kept(bx)
+            if rt is not None:
+                assert torch.equal(r, want.residual) and kept(br)
