@@ -31,7 +31,7 @@ struct NormArgs {
 // of 8 elements are read as the aligned 16-byte units that hold them and
 // shifted into place (all vectors of a row by the same `o` bytes), and
 // written the same way, with the part that lies in a lane's first unit taken
-// from the lane below.  1000 x 2563 fp16: SHIFTED us; 10.0 us with 2-byte accesses.
+// from the lane below.  1000 x 2563 fp16: 6.3 us; 10.0 us with 2-byte accesses.
 
 template <typename T> struct Units { uint32_t w[2 * sizeof(T) + 4]; };
 
@@ -149,9 +149,11 @@ struct Bounds {
 // 32-element MXFP8 block is four neighbouring lanes.  EARLY: gamma is read
 // before the row's sum is known, which shortens a row's chain of waits (64 x
 // 5120: 2.7 us, 3.3 without) but takes registers that many rows need more as
-// rows in flight (8192 x 5120, no residual: 46 us, 32 without).
+// rows in flight (8192 x 5120, no residual: 46 us, 32 without, at the four blocks
+// an SM that the launch bounds ask for there; 38 with three).
 template <typename XT, typename RT, bool HAS_R, bool ALIGNED, int NV, bool WARP_ROWS, bool EARLY>
-__global__ void __launch_bounds__(WARP_ROWS ? 128 : NV == 2 ? 512 : 1024) rms_norm_kernel(const NormArgs p, const Bounds end)
+__global__ void __launch_bounds__(WARP_ROWS ? 128 : NV == 2 ? 512 : 1024,
+                                  NV == 2 && !EARLY && !HAS_R && ALIGNED ? 4 : 1) rms_norm_kernel(const NormArgs p, const Bounds end)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -314,7 +316,7 @@ cudaError_t launch(const NormArgs &a, const Bounds &end, cudaStream_t stream)
     launch_pdl(rms_norm_kernel<XT, RT, HAS_R, ALIGNED, NV, WARP, EARLY>, dim3(grid), dim3(block), 0, stream, a, end)
     if (nvec <= 32) return BEAM_NORM(1, true, true, (rows + 3) / 4, 128);
     // unaligned rows of 1001: four vectors a lane take 156 registers (31 us for
-    // 8000 rows), a block of two vectors a thread WIDEQ
+    // 8000 rows), a block of two vectors a thread 23 us
     if (ALIGNED && nvec <= 32 * 4) return BEAM_NORM(4, true, false, (rows + 3) / 4, 128);
     const int nv = nvec <= 1024 ? 2 : 4;
     const int block = ((nvec + nv - 1) / nv + 31) / 32 * 32;
