@@ -49,8 +49,9 @@ struct Cfg {
     static constexpr int SF0 = NBUF * BN;
     static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 256;
     static constexpr int CTAS_PER_SM = BN <= 64 ? 2 : 1;
+    static constexpr int RED_LD = BN + 4;   // floats a row of a tile in shared memory: no bank met twice
     static_assert(STAGES >= 3 && SF0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory");
-    static_assert(SMEM <= 232448 && BN * kTileP * 4 <= STAGES * STAGE, "shared memory");
+    static_assert(SMEM <= 232448 && RED_LD * kTileP * 4 <= STAGES * STAGE, "shared memory");
 };
 
 // Instruction descriptor of the block-scaled kinds: bits 4-5 scale id of B,
@@ -64,11 +65,55 @@ uint32_t idesc_of(int kind, int m, int n, bool a_fp4, bool b_fp4)
            ((uint32_t)(m >> 7) << 27);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
+}
+
+// A CTA's share of a tile: every (8 split)-th group of rows of out, each the
+// sum over the cluster's FP32 tiles ([rows][LD] at `base`, COLS columns) in
+// rank order.  Four columns a lane, all ranks' loads in flight together.
+template <int COLS, int LD>
+__device__ __forceinline__ void write_tile(const MatmulArgs &p, uint32_t base, int rank, int w, int lane, int row0, int rows,
+                                           int col0, int cols)
+{
+    constexpr int LANES = COLS / 4, GROUP = 32 / LANES;   // lanes a row, rows a warp takes at once
+    const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
+    const int c = lane % LANES * 4;
+    for (int r = (rank * kEpiWarps + w) * GROUP + lane / LANES; r < rows; r += kEpiWarps * p.split * GROUP) {
+        if (c >= cols) continue;
+        const uint32_t at = base + (uint32_t)(r * LD + c) * 4u;
+        float4 v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s < p.split) v[s] = ld_cluster_f32x4(p.split > 1 ? mapa_shared(at, (uint32_t)s) : at);
+        float4 y = v[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+            if (s < p.split) y.x += v[s].x, y.y += v[s].y, y.z += v[s].z, y.w += v[s].w;
+        const float o[4] = {y.x * ga * gw, y.y * ga * gw, y.z * ga * gw, y.w * ga * gw};
+        const size_t to = (size_t)(row0 + r) * p.ldo + col0 + c;
+        if (p.dtype == BEAM_F32) {
+            float *out = static_cast<float *>(p.out) + to;
+            if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+                *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
+                continue;
+            }
+        } else {
+            uint16_t *out = static_cast<uint16_t *>(p.out) + to;
+            if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
+                *reinterpret_cast<uint2 *>(out) = p.dtype == BEAM_BF16 ? make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]))
+                                                                       : make_uint2(pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3]));
+                continue;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < cols) put(p.out, p.dtype, to + j, o[j]);
+    }
 }
 
 template <int KIND, int BN>
@@ -218,10 +263,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     if constexpr (CH == 32) tmem_ld32(taddr + c1, r);
                     else tmem_ld16(taddr + c1, r);
                     tmem_ld_wait();
-                    if (p.split > 1) {
-                        float *red = reinterpret_cast<float *>(base_ptr);   // [column][128 rows]
+                    if (p.single) {   // the ring is free: its one tile goes there, in rows of out
+                        float *red = reinterpret_cast<float *>(base_ptr);
+                        if (p.swap) {
 #pragma unroll
-                        for (int j = 0; j < CH; ++j) red[(c1 + j) * kTileP + quad * 32 + lane] = __uint_as_float(r[j]);
+                            for (int j = 0; j < CH; ++j) red[(c1 + j) * kTileP + quad * 32 + lane] = __uint_as_float(r[j]);
+                        } else {
+                            uint4 *row = reinterpret_cast<uint4 *>(red + (quad * 32 + lane) * C::RED_LD + c1);
+#pragma unroll
+                            for (int j = 0; j < CH; j += 4) row[j / 4] = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                        }
                         continue;
                     }
                     float v[CH];
@@ -255,29 +306,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
         }
     }
 
-    if (p.split > 1) {
+    if (p.single) {
+        // every CTA's FP32 tile is in its shared memory
         __syncwarp();
-        cluster_sync();   // every CTA's FP32 tile is in its shared memory
-        const int pt = first % p.p_tiles, qt = first / p.p_tiles;
+        if (p.split > 1) cluster_sync();
+        else __syncthreads();
         if (warp >= 2 && first < total) {
-            const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
-            const int tid = threadIdx.x - 64;
-            const int cols = min(BN, p.Q - qt * BN);
-            const int lo = cols * rank / p.split, hi = cols * (rank + 1) / p.split;
-            const int row = tid & 127;
-            const int prow = pt * kTileP + row;
-            for (int c = lo + (tid >> 7); c < hi; c += 2) {
-                float y = 0.f;
-                for (int r = 0; r < p.split; ++r)
-                    y += ld_cluster_f32(mapa_shared(base + (uint32_t)(c * kTileP + row) * 4u, (uint32_t)r));
-                y = y * ga * gw;
-                const int q = qt * BN + c;
-                if (prow < p.P)
-                    put(p.out, p.dtype, p.swap ? (size_t)q * p.ldo + prow : (size_t)prow * p.ldo + q, y);
-            }
+            const int pt = first % p.p_tiles, qt = first / p.p_tiles;
+            if (p.swap) write_tile<kTileP, kTileP>(p, base, rank, warp - 2, lane, qt * BN, min(BN, p.Q - qt * BN), pt * kTileP, min(kTileP, p.P - pt * kTileP));
+            else write_tile<BN, C::RED_LD>(p, base, rank, warp - 2, lane, pt * kTileP, min(kTileP, p.P - pt * kTileP), qt * BN, min(BN, p.Q - qt * BN));
         }
         __syncwarp();
-        cluster_sync();   // no CTA leaves while another may read its tile
+        if (p.split > 1) cluster_sync();   // no CTA leaves while another may read its tile
     }
     tc_fence_before();
     __syncthreads();
@@ -472,7 +512,8 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
         return fail(BEAM_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    const int ctas = a.split > 1 ? (int)tiles * a.split : (int)(tiles < slots ? tiles : slots);
+    a.single = !pair && (a.split > 1 || tiles <= slots);
+    const int ctas = a.single ? (int)tiles * a.split : slots;
     if (pair) e = launch_pair(kind, m, a, sms, s);
     else if (kind == kNv) e = launch_bn<kNv>(bn, m, a, ctas, s);
     else if (kind == kMx4) e = launch_bn<kMx4>(bn, m, a, ctas, s);

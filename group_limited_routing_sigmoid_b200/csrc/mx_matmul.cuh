@@ -40,6 +40,7 @@ struct MatmulArgs {
     int nst;               // stages of K
     int ksteps;            // MMA K steps in all
     int split;             // CTAs that share a tile's K steps (the cluster)
+    int single;            // 1: every CTA has one tile (or its share of one)
     int swap;              // 1: the A side holds the weights
     int dtype;
     int vec;               // 1: rows of out start on 16-byte boundaries
@@ -168,7 +169,48 @@ __device__ __forceinline__ void stage_columns(const float (&v)[32], uint8_t *stg
 }
 
 // Write the staged lines out: `rows` rows of `cols` columns (at most a line)
-// from out[at], rows ldo apart.  vec: 16-byte stores of whole units.
+// from out[at], rows ldo apart.  vec: every row starts on 16 bytes.  Rows that
+// do not are stored as the aligned 16-byte units they cover, each from the two
+// staged units that hold it, and their ends element by element (2-byte stores
+// of whole lines took 13 of 29 us of 1021 x 5123 x 2560).
+template <int ES>
+__device__ __forceinline__ void flush_row(const uint8_t *line, int row, int u, uint8_t *o, int cols)
+{
+    constexpr int PER = 16 / ES;
+    const auto unit = [&](int i) { return *reinterpret_cast<const uint4 *>(line + ((i ^ (row & 7)) * 16)); };
+    const auto element = [&](int c) {
+        const uint8_t *s = line + (((c / PER) ^ (row & 7)) * 16) + c % PER * ES;
+        if constexpr (ES == 4) *reinterpret_cast<uint32_t *>(o + c * 4) = *reinterpret_cast<const uint32_t *>(s);
+        else *reinterpret_cast<uint16_t *>(o + c * 2) = *reinterpret_cast<const uint16_t *>(s);
+    };
+    const int off = (int)(reinterpret_cast<uintptr_t>(o) & 15u);
+    if (off == 0) {
+        if ((u + 1) * PER <= cols) *reinterpret_cast<uint4 *>(o + u * 16) = unit(u);
+        else
+            for (int c = u * PER; c < cols; ++c) element(c);
+        return;
+    }
+    // unit u of memory: bytes 16 u - off and on of the line
+    const int head = (16 - off) / ES;                 // elements before the first whole unit
+    if (u > 0 && head + u * PER <= cols) {
+        const uint4 a = unit(u - 1), b = unit(u);
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int s = 16 - off;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+        if constexpr (ES == 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = s & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        *reinterpret_cast<uint4 *>(o + u * 16 - off) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the ends: elements before the first and past the last whole unit
+    if (u < head && u < cols) element(u);
+    const int tail = cols <= head ? cols : head + (cols - head) / PER * PER;
+    if (tail + u < cols) element(tail + u);
+}
+
 __device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dtype, void *out, size_t at, long long ldo,
                                             int rows, int cols, bool vec)
 {
@@ -176,21 +218,23 @@ __device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dt
     __syncwarp();
     uint8_t *o = static_cast<uint8_t *>(out) + at * es;
     const size_t pitch = (size_t)ldo * es;
+    const int u = lane & 7;
     if (vec && cols % per == 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3), u = lane & 7;
+            const int row = 4 * i + (lane >> 3);
             if (row < rows && u * per < cols)
                 *reinterpret_cast<uint4 *>(o + row * pitch + u * 16) =
                     *reinterpret_cast<const uint4 *>(stg + row * 128 + ((u ^ (row & 7)) * 16));
         }
     } else {
-        for (int row = 0; row < rows; ++row)
-            for (int c = lane; c < cols; c += 32) {
-                const uint8_t *s = stg + row * 128 + (((c / per) ^ (row & 7)) * 16) + c % per * es;
-                if (es == 4) *reinterpret_cast<uint32_t *>(o + row * pitch + c * 4) = *reinterpret_cast<const uint32_t *>(s);
-                else *reinterpret_cast<uint16_t *>(o + row * pitch + c * 2) = *reinterpret_cast<const uint16_t *>(s);
-            }
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            if (row >= rows) continue;
+            if (es == 4) flush_row<4>(stg + row * 128, row, u, o + row * pitch, cols);
+            else flush_row<2>(stg + row * 128, row, u, o + row * pitch, cols);
+        }
     }
     __syncwarp();
 }
