@@ -10,9 +10,9 @@
 //   warp 0      one lane loads stages: a 128-byte wide box of codes of either
 //               side (128B swizzle) and the 512-byte scale tiles that go with
 //               it, by TMA and bulk copies into a ring
-//   warp 1      one lane copies a stage's scale tiles to tensor memory
-//               (tcgen05.cp, replicated to the four lane quadrants) and issues
-//               its four MMAs
+//   warp 10     one lane copies a stage's scale tiles to tensor memory
+//               (tcgen05.cp, replicated to the four lane quadrants)
+//   warp 1      one lane issues a stage's four MMAs
 //   warps 2-9   epilogue: tensor memory to registers, tensor scales, rounding,
 //               stores
 //
@@ -47,7 +47,7 @@ struct Cfg {
     static constexpr int TMEM_COLS = BN <= 64 ? 256 : 512;
     static constexpr int NBUF = 2;
     static constexpr int SF0 = NBUF * BN;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 256;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 384;
     static constexpr int CTAS_PER_SM = BN <= 64 ? 2 : 1;
     static constexpr int RED_LD = BN + 4;   // floats a row of a tile in shared memory: no bank met twice
     static_assert(STAGES >= 3 && SF0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory");
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
     uint64_t *tfull = empty + C::STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *scaled = drain + 2;   // a stage's scales are in tensor memory (and its codes in shared)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scaled + C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl ctl{p.status, kWaitLimitNs};
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
@@ -141,12 +142,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&scaled[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
             mbar_init(smem_u32(&tempty[a]), 32 * kEpiWarps);
         }
-        mbar_init(smem_u32(drain), 1);
+        for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&drain[a]), 1);
         fence_barrier_init();
         tma_prefetch_desc(&maps.p);
         tma_prefetch_desc(&maps.q);
@@ -219,15 +221,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                 if (!mbar_wait(smem_u32(&tempty[acc]), ((uint32_t)(iter / C::NBUF) & 1u) ^ 1u, ctl)) break;
                 tc_fence_after();
                 for (int ks = ks0; ks < ks1; ++ks) {
-                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl)) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl) || !mbar_wait(smem_u32(&scaled[stage]), phase, ctl)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
-                    // a column set per ring stage: a copy never meets an
-                    // earlier stage's MMAs still reading
-                    mma_stage<KIND, 1, C::NQB>(d, sp, sq, sf, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
+                    const uint32_t sp = base + stage * C::STAGE;
+                    mma_stage<KIND, 1, C::NQB>(d, sp, sp + C::P_BYTES, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
                                                min(4, p.ksteps - ks * 4), ks == ks0);
                     any = true;
                     umma_commit(smem_u32(&empty[stage]));
@@ -238,6 +238,34 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
             if (any) {   // every MMA is complete before tensor memory is released
                 umma_commit(smem_u32(drain));
                 mbar_wait_drain(smem_u32(drain), 0, ctl.limit_ns);
+            }
+        }
+    } else if (warp == kCopyWarp) {
+        if (lane == 0) {
+            // ------------------------------------------------ scales
+            // In a thread of their own: in the MMAs' they took as long again
+            // as those (a single tile of K = 20480: NVFP4 44 -> 33 us).
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            for (int item = first; item < total && ok; item += stride) {
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    // a column set per ring stage: a copy never meets an
+                    // earlier stage's MMAs still reading
+                    copy_scales<KIND, 1, C::NQB>(base + stage * C::STAGE + C::P_BYTES + C::Q_BYTES,
+                                                 tmem + C::SF0 + stage * C::SF_COLS);
+                    any = true;
+                    umma_commit(smem_u32(&scaled[stage]));
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+            if (any) {
+                umma_commit(smem_u32(&drain[1]));
+                mbar_wait_drain(smem_u32(&drain[1]), 0, ctl.limit_ns);
             }
         }
     } else {
@@ -311,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
         __syncwarp();
         if (p.split > 1) cluster_sync();
         else __syncthreads();
-        if (warp >= 2 && first < total) {
+        if (warp >= 2 && warp < kCopyWarp && first < total) {
             const int pt = first % p.p_tiles, qt = first / p.p_tiles;
             if (p.swap) write_tile<kTileP, kTileP>(p, base, rank, warp - 2, lane, qt * BN, min(BN, p.Q - qt * BN), pt * kTileP, min(kTileP, p.P - pt * kTileP));
             else write_tile<BN, C::RED_LD>(p, base, rank, warp - 2, lane, pt * kTileP, min(kTileP, p.P - pt * kTileP), qt * BN, min(BN, p.Q - qt * BN));
@@ -512,8 +540,9 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
         return fail(BEAM_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    a.single = !pair && (a.split > 1 || tiles <= slots);
-    const int ctas = a.single ? (int)tiles * a.split : slots;
+    // weights on the A side leave tensor memory in rows of out as they are
+    a.single = !pair && (a.split > 1 || (tiles <= slots && !swap));
+    const int ctas = (int)(tiles * a.split < slots || a.split > 1 ? tiles * a.split : slots);
     if (pair) e = launch_pair(kind, m, a, sms, s);
     else if (kind == kNv) e = launch_bn<kNv>(bn, m, a, ctas, s);
     else if (kind == kMx4) e = launch_bn<kMx4>(bn, m, a, ctas, s);

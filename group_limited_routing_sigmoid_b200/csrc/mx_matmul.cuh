@@ -16,7 +16,8 @@ enum Kind { kNv = 0, kMx4 = 1, kMx8 = 2 };
 constexpr int kTileP = 128;               // rows of the A side per CTA
 constexpr int kRowBytes = 128;            // bytes of a row in a stage
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kCopyWarp = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr long long kWaitLimitNs = 2000000000ll;
 
 // 512-byte scale tiles (128 rows x 4 scales) per stage and 128 rows.
@@ -109,11 +110,9 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 }
 #undef BEAM_MMA_SCALED
 
-// One stage: its scale tiles to tensor memory, then its MMAs.  sp, sq, sf:
-// the stage's codes and scales in shared memory; tsf: its columns.
+// A stage's scale tiles (at sf in shared memory) to its columns tsf.
 template <int KIND, int CTAS, int NQB>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, uint32_t sf, uint32_t tsf, uint32_t idesc,
-                                          int steps, bool first)
+__device__ __forceinline__ void copy_scales(uint32_t sf, uint32_t tsf)
 {
     constexpr int CPS = tiles_per_stage(KIND);
     const uint32_t tsfq = tsf + CPS * 4;
@@ -123,6 +122,14 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, 
 #pragma unroll
         for (int b = 0; b < NQB; ++b) scale_copy<CTAS>(tsfq + (c * NQB + b) * 4, sf + (CPS * (1 + b) + c) * 512);
     }
+}
+
+// A stage's MMAs.  sp, sq: its codes in shared memory; tsf: its scales' columns.
+template <int KIND, int CTAS, int NQB>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, uint32_t tsf, uint32_t idesc, int steps,
+                                          bool first)
+{
+    const uint32_t tsfq = tsf + tiles_per_stage(KIND) * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (j < steps) {

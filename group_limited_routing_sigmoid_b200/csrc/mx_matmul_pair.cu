@@ -47,7 +47,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *tfull = empty + C::STAGES;
     uint64_t *tempty = tfull + 1;
     uint64_t *drain = tempty + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *scaled = drain + 2;   // a stage's scales are in both CTAs' tensor memory
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scaled + C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();   // 0 issues the MMAs
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -57,10 +58,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&scaled[s]), 1);
         }
         mbar_init(smem_u32(tfull), 1);
         mbar_init(smem_u32(tempty), 2 * 32 * kEpiWarps);
-        mbar_init(smem_u32(drain), 1);
+        for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&drain[a]), 1);
         fence_barrier_init();
         tma_prefetch_desc(&maps.p);
         tma_prefetch_desc(&maps.q);
@@ -130,13 +132,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!mbar_wait_cluster(smem_u32(tempty), (iter & 1u) ^ 1u, ctl)) break;
                 tc_fence_after();
                 for (int ks = 0; ks < p.nst; ++ks) {
-                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl)) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl) || !mbar_wait(smem_u32(&scaled[stage]), phase, ctl)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sp = base + stage * C::STAGE, sq = sp + C::HALF, sf = sq + C::HALF;
-                    mma_stage<KIND, 2, 2>(tmem, sp, sq, sf, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
+                    const uint32_t sp = base + stage * C::STAGE;
+                    mma_stage<KIND, 2, 2>(tmem, sp, sp + C::HALF, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
                                           min(4, p.ksteps - ks * 4), ks == 0);
                     any = true;
                     umma_commit_pair(smem_u32(&empty[stage]), kBoth);
@@ -145,6 +147,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (ok) umma_commit_pair(smem_u32(tfull), kBoth);
             }
             if (any) umma_commit_pair(smem_u32(drain), kBoth);
+        }
+    } else if (warp == kCopyWarp) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------ scales
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true, any = false;
+            for (int item = pair; item < total && ok; item += npairs) {
+                for (int ks = 0; ks < p.nst; ++ks) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    copy_scales<KIND, 2, 2>(base + stage * C::STAGE + 2 * C::HALF, tmem + C::SF0 + stage * C::SF_COLS);
+                    any = true;
+                    umma_commit_pair(smem_u32(&scaled[stage]), 1);
+                    if (++stage == C::STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+            if (any) umma_commit_pair(smem_u32(&drain[1]), kBoth);
         }
     } else {
         // ---------------------------------------------------- epilogue (both CTAs)
@@ -182,8 +204,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
-    // no tensor memory is released before CTA 0's MMAs are complete
-    if (warp == 1 && lane == 0 && pair < total) mbar_wait_drain(smem_u32(drain), 0, ctl.limit_ns);
+    // no tensor memory is released before CTA 0's copies and MMAs are complete
+    if (warp == 1 && lane == 0 && pair < total) {
+        mbar_wait_drain(smem_u32(drain), 0, ctl.limit_ns);
+        mbar_wait_drain(smem_u32(&drain[1]), 0, ctl.limit_ns);
+    }
     tc_fence_before();
     __syncthreads();
     __syncwarp();
