@@ -16,10 +16,22 @@
 //   warps 2-9   epilogue: tensor memory to registers, tensor scales, rounding,
 //               stores
 //
-// Where there are fewer tiles than SMs, the K steps of a tile are split over
-// the CTAs of a cluster; each leaves its FP32 tile in its own shared memory
-// and sums a share of the columns over all of them, in rank order, so results
-// do not depend on timing and no workspace is needed.
+// Where there are few tiles, the K steps of a tile are split over the CTAs of a
+// cluster; each leaves its FP32 tile in its own shared memory and writes a
+// share of the rows, summed over all of them in rank order, so results do not
+// depend on timing and no workspace is needed.
+//
+// Bound, on a B200:
+//   one sequence, NVFP4 5120 x 20480 (59 MB): 13.5 us = 4.4 TB/s.  About 3 us
+//     are launch, set-up and the sum over a cluster; the stream itself runs at
+//     5.5 TB/s (37888 x 20480: 79 us), the scales' copies taking 8% of it.
+//   64 tokens, MXFP8 x MXFP4, 20480 x 5120 (56 MB): 21.8 us = 2.7 TB/s.  Copies
+//     that spread 4-bit codes cost the TMA unit 3 clocks a row of 64 bytes of
+//     codes, as much as for 128 bytes of others, and the token rows as many
+//     again by half; and 160 tiles leave 12 of 148 SMs with two.  Weights on
+//     the B side in tiles of 192, tokens on A, took 25.6 us.
+//   L2 prefetches of the codes 6 or 12 stages ahead made all of them slower
+//     (79 -> 95 us, 27 -> 32 us).
 #include <atomic>
 
 #include "mx_matmul.cuh"
@@ -75,45 +87,67 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
 
 // A CTA's share of a tile: every (8 split)-th group of rows of out, each the
 // sum over the cluster's FP32 tiles ([rows][LD] at `base`, COLS columns) in
-// rank order.  Four columns a lane, all ranks' loads in flight together.
+// rank order.  Four columns a lane; the loads of 8 / S rows from up to S ranks
+// are in flight together, since another CTA's shared memory is some 500 clocks
+// away (row by row 1000 x 100 x 512 took 7.4 us, 6.4 us so).
+template <int COLS, int LD, int S>
+__device__ __forceinline__ void write_rows(const MatmulArgs &p, uint32_t base, int rank, int w, int lane, int row0, int rows,
+                                           int col0, int cols)
+{
+    constexpr int LANES = COLS / 4, GROUP = 32 / LANES, U = 8 / S;   // lanes a row, rows a warp takes at once
+    static_assert(LANES * GROUP == 32, "whole warps");
+    const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
+    const int c = lane % LANES * 4, step = kEpiWarps * p.split * GROUP;
+    for (int first = (rank * kEpiWarps + w) * GROUP + lane / LANES; first < rows; first += U * step) {
+        float4 v[U][S];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = first + u * step;
+            if (r >= rows || c >= cols) continue;
+            const uint32_t at = base + (uint32_t)(r * LD + c) * 4u;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (s < p.split) v[u][s] = ld_cluster_f32x4(S > 1 ? mapa_shared(at, (uint32_t)s) : at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = first + u * step;
+            if (r >= rows || c >= cols) continue;
+            float4 y = v[u][0];
+#pragma unroll
+            for (int s = 1; s < S; ++s)
+                if (s < p.split) y.x += v[u][s].x, y.y += v[u][s].y, y.z += v[u][s].z, y.w += v[u][s].w;
+            const float o[4] = {y.x * ga * gw, y.y * ga * gw, y.z * ga * gw, y.w * ga * gw};
+            const size_t to = (size_t)(row0 + r) * p.ldo + col0 + c;
+            if (p.dtype == BEAM_F32) {
+                float *out = static_cast<float *>(p.out) + to;
+                if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+                    *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
+                    continue;
+                }
+            } else {
+                uint16_t *out = static_cast<uint16_t *>(p.out) + to;
+                if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
+                    *reinterpret_cast<uint2 *>(out) = p.dtype == BEAM_BF16 ? make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]))
+                                                                           : make_uint2(pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3]));
+                    continue;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < cols) put(p.out, p.dtype, to + j, o[j]);
+        }
+    }
+}
+
 template <int COLS, int LD>
 __device__ __forceinline__ void write_tile(const MatmulArgs &p, uint32_t base, int rank, int w, int lane, int row0, int rows,
                                            int col0, int cols)
 {
-    constexpr int LANES = COLS / 4, GROUP = 32 / LANES;   // lanes a row, rows a warp takes at once
-    const float ga = p.ga ? *p.ga : 1.0f, gw = p.gw ? *p.gw : 1.0f;
-    const int c = lane % LANES * 4;
-    for (int r = (rank * kEpiWarps + w) * GROUP + lane / LANES; r < rows; r += kEpiWarps * p.split * GROUP) {
-        if (c >= cols) continue;
-        const uint32_t at = base + (uint32_t)(r * LD + c) * 4u;
-        float4 v[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-            if (s < p.split) v[s] = ld_cluster_f32x4(p.split > 1 ? mapa_shared(at, (uint32_t)s) : at);
-        float4 y = v[0];
-#pragma unroll
-        for (int s = 1; s < 8; ++s)
-            if (s < p.split) y.x += v[s].x, y.y += v[s].y, y.z += v[s].z, y.w += v[s].w;
-        const float o[4] = {y.x * ga * gw, y.y * ga * gw, y.z * ga * gw, y.w * ga * gw};
-        const size_t to = (size_t)(row0 + r) * p.ldo + col0 + c;
-        if (p.dtype == BEAM_F32) {
-            float *out = static_cast<float *>(p.out) + to;
-            if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
-                *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
-                continue;
-            }
-        } else {
-            uint16_t *out = static_cast<uint16_t *>(p.out) + to;
-            if (c + 4 <= cols && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
-                *reinterpret_cast<uint2 *>(out) = p.dtype == BEAM_BF16 ? make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]))
-                                                                       : make_uint2(pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3]));
-                continue;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < cols) put(p.out, p.dtype, to + j, o[j]);
-    }
+    if (p.split == 1) write_rows<COLS, LD, 1>(p, base, rank, w, lane, row0, rows, col0, cols);
+    else if (p.split == 2) write_rows<COLS, LD, 2>(p, base, rank, w, lane, row0, rows, col0, cols);
+    else if (p.split <= 4) write_rows<COLS, LD, 4>(p, base, rank, w, lane, row0, rows, col0, cols);
+    else write_rows<COLS, LD, 8>(p, base, rank, w, lane, row0, rows, col0, cols);
 }
 
 template <int KIND, int BN>
@@ -194,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     tma_load_2d(sp, &maps.p, ks * kRowBytes, pt * kTileP, fb, pol_p);
                     tma_load_2d(sq, &maps.q, ks * kRowBytes, qt * BN, fb, pol_q);
                     tma_load_3d(sf, &maps.sp, ks * CPS, pt, fb);
-                    tma_load_3d(sf + CPS * 512, &maps.sq, ks * CPS, qt, fb);
+                    tma_load_3d(sf + CPS * 512, &maps.sq, ks * CPS, qt * BN >> 7, fb);
                     ++issued;
                     if (++stage == C::STAGES) stage = 0, phase ^= 1u;
                 }
@@ -218,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
             for (int item = first; item < total && ok; item += stride, ++iter) {
                 const int acc = iter % C::NBUF;
                 const uint32_t d = tmem + acc * BN;
+                const uint32_t qcol = BN == 64 ? scale_column(item / p.p_tiles * BN) : 0u;   // smaller: one tile of B
                 if (!mbar_wait(smem_u32(&tempty[acc]), ((uint32_t)(iter / C::NBUF) & 1u) ^ 1u, ctl)) break;
                 tc_fence_after();
                 for (int ks = ks0; ks < ks1; ++ks) {
@@ -227,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     }
                     tc_fence_after();
                     const uint32_t sp = base + stage * C::STAGE;
-                    mma_stage<KIND, 1, C::NQB>(d, sp, sp + C::P_BYTES, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
+                    mma_stage<KIND, 1, C::NQB>(d, sp, sp + C::P_BYTES, tmem + C::SF0 + stage * C::SF_COLS, qcol, p.idesc,
                                                min(4, p.ksteps - ks * 4), ks == ks0);
                     any = true;
                     umma_commit(smem_u32(&empty[stage]));
@@ -442,6 +477,64 @@ cudaError_t launch_bn(int bn, const Maps &m, const MatmulArgs &a, int ctas, cuda
     }
 }
 
+// Clusters of 1 to 8 CTAs that a B200 holds at once, at one and two CTAs an SM
+// (cudaOccupancyMaxActiveClusters with these kernels' threads and shared
+// memory).  More clusters than fit only wait for their turn.
+constexpr int kClusters[2][8] = {{148, 74, 45, 33, 26, 22, 15, 15}, {296, 148, 93, 71, 56, 45, 37, 33}};
+
+struct Plan {
+    int bn, split;
+    bool pair;
+    long long cost;   // ns
+};
+
+// Tile width and split of K with the least estimated time.  The estimate: 2.5
+// us of launch; a tile's set-up and epilogue; its stages one after another (a
+// stage of a lone CTA waits on its loads and scale copies, 0.3 us + 2 ns a
+// column, longer where two CTAs share an SM); the sum over a cluster; and all
+// that as often as there are waves of tiles.  It was fitted to tiles of 32 to
+// 128 columns split 1 to 8 times (500 x 500 x 512: 5.0 us at 64 columns, 6.2 at
+// 128; 300 x 1000 x 5120: 9.9 us split 4 ways, 18.3 whole; 1 x 5120 x 20480:
+// 13.5 us split 6 ways, 16.3 four ways, 25 two ways) and pairs (2048 x 5120 x
+// 5120 MXFP8 x MXFP4: 50 us, 70 on single CTAs; 1021 x 5123 x 2560: 20.7 us,
+// 17.5 on single CTAs, whose many tiles hide the odd rows' stores better).
+Plan plan(int kind, int P, int Q, int nst, bool swap, bool vec, int sms)
+{
+    const long long p_tiles = (P + kTileP - 1) / kTileP;
+    Plan best{0, 1, false, 0};
+    const auto offer = [&](int bn, int split, bool pair, long long cost) {
+        if (best.bn == 0 || cost < best.cost) best = Plan{bn, split, pair, cost};
+    };
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        if (bn < 64 && bn < Q) continue;        // one tile of B, or scales at even columns
+        const long long tiles = p_tiles * ((Q + bn - 1) / bn);
+        const int per_sm = bn <= 64 ? 2 : 1;
+        const long long fixed = 900 + 12 * bn;
+        if (tiles > (long long)sms * per_sm) {   // persistent, the epilogue beside the next tile
+            if (bn < 128 && !swap) continue;     // whose stores are then by columns
+            const long long waves = (tiles + sms * per_sm - 1) / (sms * per_sm);
+            offer(bn, 1, false, 2500 + fixed + waves * (nst * 410ll * per_sm + (vec ? 0 : 800)));
+        } else {
+            for (int s = 1; s <= 8 && s <= nst; ++s) {
+                const long long waves = (tiles + kClusters[per_sm - 1][s - 1] - 1) / kClusters[per_sm - 1][s - 1];
+                const long long ctas = tiles * s < (long long)sms * per_sm ? tiles * s : (long long)sms * per_sm;
+                // CTAs an SM, in thousandths: 8-bit stages mostly wait, 4-bit
+                // ones (twice the K) are held up by the SM's other CTA
+                const long long mean = ctas > sms ? ctas * 1000 / sms : 1000;
+                const long long share = kind == kMx8 ? mean : (mean + (mean + 999) / 1000 * 1000) / 2;
+                const long long stage = (300 + 2 * bn) * share / 1000;
+                offer(bn, s, false, 500 + waves * (2000 + fixed + (s > 1 ? 300 + 100 * s : 0) + (nst + s - 1) / s * stage));
+            }
+        }
+        if (bn >= Q) break;
+    }
+    if (!swap && P > 128 && Q > 128) {
+        const long long tiles = (long long)((P + 255) / 256) * ((Q + 255) / 256), waves = (tiles + sms / 2 - 1) / (sms / 2);
+        offer(256, 1, true, 5000 + waves * (nst * 500ll + (vec ? 0 : 2900)));
+    }
+    return best;
+}
+
 // Device address of the status word, looked up once per device.
 std::atomic<int *> g_status_ptr[64];
 
@@ -508,23 +601,13 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
     a.nst = (K + stage_k(kind) - 1) / stage_k(kind);
     a.ksteps = K / step_k(kind);
     const int n4 = (K / block_of(a_format) + 3) / 4;
-    int bn = 16;
-    while (bn < a.Q && bn < 128) bn *= 2;
-    a.p_tiles = (a.P + kTileP - 1) / kTileP;
+    const Plan how = plan(kind, a.P, a.Q, a.nst, swap, a.vec != 0, sms);
+    const int bn = how.bn, slots = sms * (bn <= 64 ? 2 : 1);
+    const bool pair = how.pair;
+    a.split = how.split;
+    a.p_tiles = (a.P + (pair ? 255 : kTileP - 1)) / (pair ? 256 : kTileP);
     a.q_tiles = (a.Q + bn - 1) / bn;
     const long long tiles = (long long)a.p_tiles * a.q_tiles;
-    // pairs of CTAs (256 x 256 tiles) where they fill the SMs
-    const int pair_p = (a.P + 255) / 256, pair_q = (a.Q + 255) / 256;
-    const bool pair = !swap && (long long)pair_p * pair_q * 2 >= sms;
-    a.split = 1;
-    const int slots = sms * (bn <= 64 ? 2 : 1);
-    if (pair) {
-        a.p_tiles = pair_p;
-        a.q_tiles = pair_q;
-        bn = 256;
-    } else {
-        while (a.split < 8 && tiles * a.split * 2 <= slots && a.split * 2 <= a.nst) a.split *= 2;
-    }
     const bool p_fp4 = (swap ? w_format : a_format) != BEAM_MXFP8, q_fp4 = (swap ? a_format : w_format) != BEAM_MXFP8;
     const bool p_spread = kind == kMx8 && p_fp4, q_spread = kind == kMx8 && q_fp4;
     a.idesc = idesc_of(kind, pair ? 256 : 128, bn, p_fp4, q_fp4);

@@ -124,12 +124,19 @@ __device__ __forceinline__ void copy_scales(uint32_t sf, uint32_t tsf)
     }
 }
 
-// A stage's MMAs.  sp, sq: its codes in shared memory; tsf: its scales' columns.
+// The first column, within its 128-row block's four, of the scales of a B tile
+// that starts at `row`, a multiple of 64: 32 rows' scales are one column.  (An
+// odd column -- a tile at an odd multiple of 32 rows -- is no scale address
+// that the MMA takes.)
+__device__ __forceinline__ uint32_t scale_column(int row) { return (uint32_t)(row >> 5) & 2u; }
+
+// A stage's MMAs.  sp, sq: its codes in shared memory; tsf: its scales'
+// columns; qcol: scale_column of the B tile.
 template <int KIND, int CTAS, int NQB>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, uint32_t tsf, uint32_t idesc, int steps,
-                                          bool first)
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sp, uint32_t sq, uint32_t tsf, uint32_t qcol, uint32_t idesc,
+                                          int steps, bool first)
 {
-    const uint32_t tsfq = tsf + tiles_per_stage(KIND) * 4;
+    const uint32_t tsfq = tsf + tiles_per_stage(KIND) * 4 + qcol;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (j < steps) {
@@ -185,37 +192,42 @@ __device__ __forceinline__ void flush_row(const uint8_t *line, int row, int u, u
 {
     constexpr int PER = 16 / ES;
     const auto unit = [&](int i) { return *reinterpret_cast<const uint4 *>(line + ((i ^ (row & 7)) * 16)); };
-    const auto element = [&](int c) {
+    const auto value = [&](int c) -> uint32_t {
         const uint8_t *s = line + (((c / PER) ^ (row & 7)) * 16) + c % PER * ES;
-        if constexpr (ES == 4) *reinterpret_cast<uint32_t *>(o + c * 4) = *reinterpret_cast<const uint32_t *>(s);
-        else *reinterpret_cast<uint16_t *>(o + c * 2) = *reinterpret_cast<const uint16_t *>(s);
+        if constexpr (ES == 4) return *reinterpret_cast<const uint32_t *>(s);
+        else return *reinterpret_cast<const uint16_t *>(s);
+    };
+    const auto store = [&](int c, uint32_t v) {
+        if constexpr (ES == 4) *reinterpret_cast<uint32_t *>(o + c * 4) = v;
+        else *reinterpret_cast<uint16_t *>(o + c * 2) = (uint16_t)v;
     };
     const int off = (int)(reinterpret_cast<uintptr_t>(o) & 15u);
     if (off == 0) {
         if ((u + 1) * PER <= cols) *reinterpret_cast<uint4 *>(o + u * 16) = unit(u);
         else
-            for (int c = u * PER; c < cols; ++c) element(c);
+            for (int c = u * PER; c < cols; ++c) store(c, value(c));
         return;
     }
-    // unit u of memory: bytes 16 u - off and on of the line
+    // unit u of memory: bytes 16 u - off and on of the line; its ends, before
+    // the first and past the last whole unit, element by element.  All reads
+    // first, so that the rows of an unrolled loop overlap.
     const int head = (16 - off) / ES;                 // elements before the first whole unit
-    if (u > 0 && head + u * PER <= cols) {
-        const uint4 a = unit(u - 1), b = unit(u);
-        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const int s = 16 - off;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
-        if constexpr (ES == 2)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = s & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-        *reinterpret_cast<uint4 *>(o + u * 16 - off) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    // the ends: elements before the first and past the last whole unit
-    if (u < head && u < cols) element(u);
     const int tail = cols <= head ? cols : head + (cols - head) / PER * PER;
-    if (tail + u < cols) element(tail + u);
+    const uint4 a = unit(u > 0 ? u - 1 : 0), b = unit(u);
+    const int t = min(tail + u, 8 * PER - 1);
+    const uint32_t first = value(u), last = value(t);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int s = 16 - off;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+    if constexpr (ES == 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = s & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    if (u > 0 && head + u * PER <= cols) *reinterpret_cast<uint4 *>(o + u * 16 - off) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (u < head && u < cols) store(u, first);
+    if (tail + u < cols) store(tail + u, last);
 }
 
 __device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dtype, void *out, size_t at, long long ldo,
@@ -235,7 +247,7 @@ __device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dt
                     *reinterpret_cast<const uint4 *>(stg + row * 128 + ((u ^ (row & 7)) * 16));
         }
     } else {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 8; ++i) {
             const int row = 4 * i + (lane >> 3);
             if (row >= rows) continue;

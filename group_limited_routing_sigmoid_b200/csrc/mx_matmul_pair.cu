@@ -138,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t sp = base + stage * C::STAGE;
-                    mma_stage<KIND, 2, 2>(tmem, sp, sp + C::HALF, tmem + C::SF0 + stage * C::SF_COLS, p.idesc,
+                    mma_stage<KIND, 2, 2>(tmem, sp, sp + C::HALF, tmem + C::SF0 + stage * C::SF_COLS, 0, p.idesc,
                                           min(4, p.ksteps - ks * 4), ks == 0);
                     any = true;
                     umma_commit_pair(smem_u32(&empty[stage]), kBoth);

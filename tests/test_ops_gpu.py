@@ -660,3 +660,57 @@ def test_norm_writes_its_rows_alone(xt, rt, T, H):
             assert torch.equal(bo[:, off:off + H], want.out) and kept(bo) and kept(bx)
             if rt is not None:
                 assert torch.equal(r, want.residual) and kept(br)
+
+
+@pytest.mark.parametrize("af,wf", PAIRS)
+@pytest.mark.parametrize("T,N", [(1, 1280), (16, 1281), (17, 1505), (64, 2000), (65, 1600), (128, 3333), (128, 5120)])
+def test_product_wide_tiles(af, wf, T, N):
+    """Few tokens against many weight rows."""
+    K = 640
+    a, av = operand(T, K, af, T, 2)
+    w, wv = operand(N, K, wf, N, 2)
+    out = torch.full((T + 1, N + 3), 7.0, dtype=torch.float32, device="cuda")
+    ops.mx_matmul(a, w, torch.float32, out=out[:T, :N])
+    assert ops.ops_status() == 0
+    check_product(out[:T, :N], torch.float32, av, wv, K)
+    assert (out[T] == 7.0).all() and (out[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("af,wf", PAIRS)
+@pytest.mark.parametrize("T,N", [(2100, 1200), (1024, 2565), (1021, 5123), (600, 4097), (4096, 513), (1300, 3500)])
+def test_product_pair_tiles(af, wf, T, N):
+    """Pairs of CTAs with every tile width, whole numbers (exact in any order), aligned and odd rows of out."""
+    K = 256
+    rng = np.random.default_rng(T)
+    opnds, vals = [], []
+    for rows, fmt in ((T, af), (N, wf)):
+        e = rng.integers(0, 3, (rows, K)).astype(float) * rng.choice([-1.0, 1.0], (rows, K))
+        one = 0x38 if fmt == "nvfp4" else 127
+        up = rng.integers(0, 2, (rows, K // R.BLOCK[fmt]))
+        sb = (one + up * (8 if fmt == "nvfp4" else 1)).astype(np.uint8)
+        opnds.append(ops.MxTensor(torch.from_numpy(R.codes(e, fmt)).cuda(), torch.from_numpy(R.tile(sb)).cuda(), fmt, "tiled", rows, K))
+        vals.append(R.values(e, sb, fmt))
+    want = vals[0] @ vals[1].T
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        out = torch.full((T, N + 1), 7.0, dtype=dtype, device="cuda")
+        ops.mx_matmul(*opnds, dtype, out=out[:, :N])
+        assert ops.ops_status() == 0
+        np.testing.assert_array_equal(out[:, :N].float().cpu().numpy(), torch.from_numpy(want).to(dtype).float().numpy())
+        assert (out[:, N] == 7.0).all()
+        assert torch.equal(ops.mx_matmul(*opnds, dtype), out[:, :N])
+
+
+@pytest.mark.parametrize("af,wf", PAIRS)
+@pytest.mark.parametrize("T,N,K", [(150, 150, 1280), (129, 449, 256), (500, 500, 512), (1000, 100, 512), (90, 140, 1152),
+                                   (200, 2000, 1024), (3000, 300, 256), (333, 65, 768), (8200, 70, 256)])
+def test_product_of_middling_sizes(af, wf, T, N, K):
+    """Tiles of 64 columns that start in the middle of a 128-row block of scales, split 1 to 8 ways."""
+    a, av = operand(T, K, af, T, 2)
+    w, wv = operand(N, K, wf, N, 2)
+    out = torch.full((T + 1, N + 3), 7.0, dtype=torch.float16, device="cuda")
+    ops.mx_matmul(a, w, torch.float16, out=out[:T, :N])
+    y = ops.mx_matmul(a, w, torch.float32)
+    assert ops.ops_status() == 0
+    check_product(y, torch.float32, av, wv, K)
+    assert torch.equal(out[:T, :N], y.half())
+    assert (out[T] == 7.0).all() and (out[:, N:] == 7.0).all()
