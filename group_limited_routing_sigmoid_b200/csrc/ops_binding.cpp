@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -30,7 +31,9 @@ struct Library {
     decltype(&beam_ops_error) error;
 } lib;
 
-PyObject *beam_error = nullptr;   // BeamMoEError
+// BeamMoEError, NormResult and MxTensor (named tuples)
+PyObject *beam_error = nullptr;
+PyTypeObject *norm_result = nullptr, *mx_tensor = nullptr;
 
 // A Python exception is set.
 struct Raised {};
@@ -140,12 +143,19 @@ struct Rows {
     }
 };
 
+// A new tensor on first's device: the CUDA allocation itself, half the time of
+// the dispatched at::empty.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &first)
+{
+    return at::Tensor(at::detail::empty_cuda(sizes, type, first.device(), c10::nullopt));
+}
+
 // An output matrix: the caller's (checked) or a new one.
 at::Tensor output(PyObject *given, const char *name, long long rows, long long cols, int code, const at::Tensor &first,
                   Rows &r)
 {
     if (given == Py_None) {
-        at::Tensor t = at::empty({rows, cols}, at::TensorOptions().dtype(scalar_type(code)).device(first.device()));
+        at::Tensor t = fresh({rows, cols}, scalar_type(code), first);
         r.p = t.data_ptr(), r.rows = rows, r.cols = cols, r.ld = cols, r.code = code;
         return t;
     }
@@ -214,9 +224,8 @@ Operand new_operand(PyObject *codes, PyObject *scales, int format, int layout, l
     Operand o;
     const long long n = scale_count(format, rows, K, layout);
     if (codes == Py_None) {
-        const auto opt = at::TensorOptions().dtype(at::kByte).device(first.device());
-        o.codes = at::empty({rows, format == BEAM_MXFP8 ? K : K / 2}, opt);
-        o.scales = layout == BEAM_SCALES_ROWS ? at::empty({rows, K / block(format)}, opt) : at::empty({n}, opt);
+        o.codes = fresh({rows, format == BEAM_MXFP8 ? K : K / 2}, at::kByte, first);
+        o.scales = layout == BEAM_SCALES_ROWS ? fresh({rows, K / block(format)}, at::kByte, first) : fresh({n}, at::kByte, first);
         o.c = static_cast<uint8_t *>(o.codes.data_ptr());
         o.s = static_cast<uint8_t *>(o.scales.data_ptr());
     } else {
@@ -233,10 +242,22 @@ PyObject *wrap_or_none(const at::Tensor &t)
     return THPVariable_Wrap(t);
 }
 
-// Steals the references of `items`.
-PyObject *pack(std::initializer_list<PyObject *> items)
+PyObject *none()
 {
-    PyObject *t = PyTuple_New((Py_ssize_t)items.size());
+    Py_INCREF(Py_None);
+    return Py_None;
+}
+
+PyObject *same(PyObject *o)
+{
+    Py_INCREF(o);
+    return o;
+}
+
+// A tuple, or one of the named ones.  Steals the references of `items`.
+PyObject *pack(std::initializer_list<PyObject *> items, PyTypeObject *type = nullptr)
+{
+    PyObject *t = type ? type->tp_alloc(type, (Py_ssize_t)items.size()) : PyTuple_New((Py_ssize_t)items.size());
     Py_ssize_t i = 0;
     for (PyObject *o : items) {
         if (!o || !t) {
@@ -270,15 +291,23 @@ PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// x, gamma, residual, alpha, beta, eps, dtype, quantize, layout, out, residual_out, want_out, codes, scales
-// -> out, residual_out, codes, scales, T, H
+// The MxTensor of an operand; format and layout are given as the strings it holds.
+PyObject *pack_operand(const Operand &q, PyObject *format, PyObject *layout, long long rows, long long K, const at::Tensor &scale)
+{
+    return pack({THPVariable_Wrap(q.codes), THPVariable_Wrap(q.scales), same(format), same(layout), PyLong_FromLongLong(rows),
+                 PyLong_FromLongLong(K), wrap_or_none(scale)},
+                mx_tensor);
+}
+
+// x, gamma, residual, alpha, beta, eps, dtype, quantize (None or the format's name), layout, its name, out,
+// residual_out, want_out, codes, scales -> NormResult
 PyObject *rms_norm(PyObject *const *a, Py_ssize_t n)
 {
-    need(n, 14);
+    need(n, 15);
     const at::Tensor &x = tensor(a[0], "x", nullptr);
     const Rows xr(x, "x");
     const int T = xr.height("x"), H = xr.columns("x"), dtype = small_integer(a[6]), layout = small_integer(a[8]);
-    const bool quantize = a[7] == Py_True, want_out = a[11] == Py_True;
+    const bool quantize = a[7] != Py_None, want_out = a[12] == Py_True;
     Rows r, ro, o;
     at::Tensor residual_out, out;
     const On on(x);
@@ -288,15 +317,15 @@ PyObject *rms_norm(PyObject *const *a, Py_ssize_t n)
         r = Rows(t, "residual");
         if (r.rows != T || r.cols != H || (r.code != BEAM_F32 && r.code != xr.code))
             raise_type("%s: expected x's shape in fp32 or x's type, got %s", "residual", shape_of(t));
-        residual_out = output(a[10], "residual_out", T, H, r.code, x, ro);
+        residual_out = output(a[11], "residual_out", T, H, r.code, x, ro);
     }
-    if (want_out) out = output(a[9], "out", T, H, dtype, x, o);
+    if (want_out) out = output(a[10], "out", T, H, dtype, x, o);
     Operand q;
-    if (quantize) q = new_operand(a[12], a[13], BEAM_MXFP8, layout, T, H, x);
+    if (quantize) q = new_operand(a[13], a[14], BEAM_MXFP8, layout, T, H, x);
     check(lib.rms_norm(on.stream, xr.p, xr.code, xr.ld, r.p, r.code, r.ld, ro.p, ro.ld, real(a[3]), real(a[4]), gamma,
                        real(a[5]), T, H, o.p, dtype, o.ld, q.c, q.s, layout));
-    return pack({wrap_or_none(out), wrap_or_none(residual_out), wrap_or_none(q.codes), wrap_or_none(q.scales),
-                 PyLong_FromLong(T), PyLong_FromLong(H)});
+    PyObject *operand = quantize ? pack_operand(q, a[7], a[9], T, H, at::Tensor()) : none();
+    return pack({wrap_or_none(out), wrap_or_none(residual_out), operand}, norm_result);
 }
 
 // x, out -> out
@@ -304,7 +333,7 @@ at::Tensor find_scale(const at::Tensor &x, const Rows &r, PyObject *given, const
 {
     at::Tensor out;
     if (given == Py_None) {
-        out = at::empty({1}, at::TensorOptions().dtype(at::kFloat).device(x.device()));
+        out = fresh({1}, at::kFloat, x);
     } else {
         flat<float>(given, "out", at::kFloat, 1, &x);
         out = THPVariable_Unpack(given);
@@ -322,10 +351,10 @@ PyObject *tensor_scale(PyObject *const *a, Py_ssize_t n)
     return THPVariable_Wrap(find_scale(x, r, a[1], on));
 }
 
-// x, format, layout, tensor_scale, codes, scales -> codes, scales, tensor_scale, rows, K
+// x, format, layout, tensor_scale, codes, scales, the format's and the layout's names -> MxTensor
 PyObject *quantize(PyObject *const *a, Py_ssize_t n)
 {
-    need(n, 6);
+    need(n, 8);
     const at::Tensor &x = tensor(a[0], "x", nullptr);
     const Rows r(x, "x");
     const int format = small_integer(a[1]), layout = small_integer(a[2]);
@@ -343,8 +372,7 @@ PyObject *quantize(PyObject *const *a, Py_ssize_t n)
         g = static_cast<const float *>(scale.data_ptr());
     }
     check(lib.quantize(on.stream, r.p, r.code, r.rows, r.columns("x"), r.ld, format, layout, g, q.c, q.s));
-    return pack({THPVariable_Wrap(q.codes), THPVariable_Wrap(q.scales), wrap_or_none(scale), PyLong_FromLongLong(r.rows),
-                 PyLong_FromLongLong(r.cols)});
+    return pack_operand(q, a[6], a[7], r.rows, r.cols, scale);
 }
 
 // codes, scales, tensor_scale, format, layout, rows, K, dtype, out -> out
@@ -376,8 +404,7 @@ PyObject *tile_scales(PyObject *const *a, Py_ssize_t n)
     const at::Tensor &scales = tensor(a[0], "scales", nullptr);
     const uint8_t *s = flat<uint8_t>(a[0], "scales", at::kByte, scale_count(format, rows, K, BEAM_SCALES_ROWS), nullptr);
     const On on(scales);
-    at::Tensor out = at::empty({scale_count(format, rows, K, BEAM_SCALES_TILED)},
-                               at::TensorOptions().dtype(at::kByte).device(scales.device()));
+    at::Tensor out = fresh({scale_count(format, rows, K, BEAM_SCALES_TILED)}, at::kByte, scales);
     check(lib.tile_scales(on.stream, format, s, rows, K, static_cast<uint8_t *>(out.data_ptr())));
     return THPVariable_Wrap(out);
 }
@@ -415,13 +442,13 @@ PyObject *route_scores(PyObject *const *a, Py_ssize_t n)
     const float *bias = flat_or_null<float>(a[3], "bias", at::kFloat, E, &l);
     at::Tensor idx, w;
     if (a[9] == Py_None) {
-        idx = at::empty({T, k}, at::TensorOptions().dtype(at::kInt).device(l.device()));
+        idx = fresh({T, k}, at::kInt, l);
     } else {
         flat<int32_t>(a[9], "idx", at::kInt, T * k, &l);
         idx = THPVariable_Unpack(a[9]);
     }
     if (a[10] == Py_None) {
-        w = at::empty({T, k}, at::TensorOptions().dtype(at::kFloat).device(l.device()));
+        w = fresh({T, k}, at::kFloat, l);
     } else {
         flat<float>(a[10], "w", at::kFloat, T * k, &l);
         w = THPVariable_Unpack(a[10]);
@@ -434,16 +461,21 @@ PyObject *route_scores(PyObject *const *a, Py_ssize_t n)
     return pack({THPVariable_Wrap(idx), THPVariable_Wrap(w)});
 }
 
-// BeamMoEError, then the addresses of the library's functions in Library's order
+// BeamMoEError, NormResult, MxTensor, then the addresses of the library's functions in Library's order
 PyObject *bind(PyObject *const *a, Py_ssize_t n)
 {
-    need(n, 1 + sizeof(Library) / sizeof(void *));
-    void *p[sizeof(Library) / sizeof(void *)];
-    for (Py_ssize_t i = 1; i < n; ++i) p[i - 1] = reinterpret_cast<void *>(integer(a[i]));
+    constexpr Py_ssize_t types = 3, functions = sizeof(Library) / sizeof(void *);
+    need(n, types + functions);
+    for (Py_ssize_t i = 1; i < types; ++i)
+        if (!PyType_Check(a[i]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject *>(a[i]), &PyTuple_Type))
+            raise_type("%s: %s", "bind", "expected types of tuples");
+    void *p[functions];
+    for (Py_ssize_t i = 0; i < functions; ++i) p[i] = reinterpret_cast<void *>(integer(a[types + i]));
     memcpy(&lib, p, sizeof(lib));
-    Py_INCREF(a[0]);
-    Py_XDECREF(beam_error);
+    for (Py_ssize_t i = 0; i < types; ++i) Py_INCREF(a[i]);   // for good
     beam_error = a[0];
+    norm_result = reinterpret_cast<PyTypeObject *>(a[1]);
+    mx_tensor = reinterpret_cast<PyTypeObject *>(a[2]);
     Py_RETURN_NONE;
 }
 

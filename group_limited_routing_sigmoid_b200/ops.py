@@ -77,7 +77,7 @@ def _native():
         spec = importlib.util.spec_from_file_location(__package__ + "._ops_binding", OPS_BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(BeamMoEError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        module.bind(BeamMoEError, NormResult, MxTensor, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.beam_rms_norm, lib.beam_mx_tensor_scale, lib.beam_mx_quantize, lib.beam_mx_dequantize,
             lib.beam_mx_tile_scales, lib.beam_mx_matmul, lib.beam_route_scores, lib.beam_ops_error)))
         _binding = module
@@ -99,10 +99,16 @@ def _elsewhere(stream, f, *args):
             stream = torch.cuda.ExternalStream(handle, device=device)
         with torch.cuda.stream(stream):
             result = f(*args)
-        for t in (*args, *(result if isinstance(result, tuple) else (result,))):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
+        _used(stream, *args, result)
         return result
+
+
+def _used(stream, *values):
+    for v in values:
+        if isinstance(v, torch.Tensor) and v.is_cuda:
+            v.record_stream(stream)
+        elif isinstance(v, tuple):
+            _used(stream, *v)
 
 
 def ops_status(device=None, stream=None) -> int:
@@ -163,10 +169,9 @@ def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale
     if f != 0 and tensor_scale is not None:
         raise ValueError(f"{format} has no tensor scale")
     q = (_binding or _native()).quantize
-    codes, scales, tensor_scale, rows, K = (
-        q(x, f, lay, tensor_scale, codes, scales) if stream is None else
-        _elsewhere(stream, q, x, f, lay, tensor_scale, codes, scales))
-    return MxTensor(codes, scales, format, layout, rows, K, tensor_scale)
+    if stream is None:
+        return q(x, f, lay, tensor_scale, codes, scales, format, layout)
+    return _elsewhere(stream, q, x, f, lay, tensor_scale, codes, scales, format, layout)
 
 
 def mx_dequantize(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -227,12 +232,11 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tens
         codes, scales = _given(quantized, "quantized", quantize, layout, x)
     f = (_binding or _native()).rms_norm
     d, lay = _key(DTYPES, dtype, "dtype"), _key(LAYOUTS, layout, "layout")
-    args = (x, gamma, residual, alpha, beta, eps, d, quantize is not None, lay, out, residual_out, bool(want_out), codes,
-            scales)
-    out, residual_out, codes, scales, T, H = f(*args) if stream is None else _elsewhere(stream, f, *args)
-    if quantize is None:
-        return NormResult(out, residual_out, None)
-    return NormResult(out, residual_out, MxTensor(codes, scales, quantize, layout, T, H))
+    want_out = bool(want_out)
+    if stream is None:
+        return f(x, gamma, residual, alpha, beta, eps, d, quantize, lay, layout, out, residual_out, want_out, codes, scales)
+    return _elsewhere(stream, f, x, gamma, residual, alpha, beta, eps, d, quantize, lay, layout, out, residual_out, want_out,
+                      codes, scales)
 
 
 def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias: Optional[torch.Tensor] = None,

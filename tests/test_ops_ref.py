@@ -209,8 +209,9 @@ def test_binding_turns_refusals_into_exceptions():
     """The compiled binding's own checks: what is no tensor, wrong counts, integers and reals out of place."""
     f = ops._native()
     x = torch.zeros(4, 64)
-    for call, args in ((f.quantize, (x, 1)), (f.quantize, (3, 1, 0, None, None, None)), (f.quantize, (None,) * 6),
-                       (f.rms_norm, (x,) * 14), (f.matmul, ("a",) * 13), (f.dequantize, (x, x, None, 1, 0, 4, "K", 0, None)),
+    for call, args in ((f.quantize, (x, 1)), (f.quantize, (3, 1, 0, None, None, None, "mxfp4", "rows")),
+                       (f.quantize, (None,) * 8),
+                       (f.rms_norm, (x,) * 15), (f.matmul, ("a",) * 13), (f.dequantize, (x, x, None, 1, 0, 4, "K", 0, None)),
                        (f.tile_scales, (x, 1, 2.5, 64)), (f.route_scores, (x,) * 11), (f.tensor_scale, (x, None))):
         with pytest.raises(TypeError):
             call(*args)
