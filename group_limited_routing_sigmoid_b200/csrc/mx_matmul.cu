@@ -491,8 +491,8 @@ struct Plan {
 // Tile width and split of K with the least estimated time.  The estimate: 2.5
 // us of launch; a tile's set-up and epilogue; its stages one after another (a
 // stage of a lone CTA waits on its loads and scale copies, 0.3 us + 2 ns a
-// column, longer where two CTAs share an SM); the sum over a cluster; and all
-// that as often as there are waves of tiles.  It was fitted to tiles of 32 to
+// column, longer where two CTAs share an SM); the sum over a cluster; and for
+// more tiles than CTAs the waves of them.  It was fitted to tiles of 32 to
 // 128 columns split 1 to 8 times (500 x 500 x 512: 5.0 us at 64 columns, 6.2 at
 // 128; 300 x 1000 x 5120: 9.9 us split 4 ways, 18.3 whole; 1 x 5120 x 20480:
 // 13.5 us split 6 ways, 16.3 four ways, 25 two ways) and pairs (2048 x 5120 x
@@ -515,15 +515,14 @@ Plan plan(int kind, int P, int Q, int nst, bool swap, bool vec, int sms)
             const long long waves = (tiles + sms * per_sm - 1) / (sms * per_sm);
             offer(bn, 1, false, 2500 + fixed + waves * (nst * 410ll * per_sm + (vec ? 0 : 800)));
         } else {
-            for (int s = 1; s <= 8 && s <= nst; ++s) {
-                const long long waves = (tiles + kClusters[per_sm - 1][s - 1] - 1) / kClusters[per_sm - 1][s - 1];
-                const long long ctas = tiles * s < (long long)sms * per_sm ? tiles * s : (long long)sms * per_sm;
+            // clusters that all fit at once
+            for (int s = 1; s <= 8 && s <= nst && tiles <= kClusters[per_sm - 1][s - 1]; ++s) {
                 // CTAs an SM, in thousandths: 8-bit stages mostly wait, 4-bit
                 // ones (twice the K) are held up by the SM's other CTA
-                const long long mean = ctas > sms ? ctas * 1000 / sms : 1000;
-                const long long share = kind == kMx8 ? mean : (mean + (mean + 999) / 1000 * 1000) / 2;
-                const long long stage = (300 + 2 * bn) * share / 1000;
-                offer(bn, s, false, 500 + waves * (2000 + fixed + (s > 1 ? 300 + 100 * s : 0) + (nst + s - 1) / s * stage));
+                const int ctas = (int)tiles * s, mean = ctas > sms ? ctas * 1000 / sms : 1000;
+                const int share = kind == kMx8 || mean == 1000 ? mean : (mean + 2000) / 2;
+                const int stage = (300 + 2 * bn) * share / 1000;
+                offer(bn, s, false, 2500 + fixed + (s > 1 ? 300 + 100 * s : 0) + (long long)((nst + s - 1) / s) * stage);
             }
         }
         if (bn >= Q) break;

@@ -28,7 +28,7 @@ constexpr int kChunk = 16;         // elements a lane takes at a time
 constexpr int kAhead = 2;          // chunks a lane loads at once
 constexpr int kCluster = 8;
 // Up to this many chunks one cluster finds the tensor scale, without the
-// memset that atomics want before them (64 x 5120: AMAXO us, 4.4 us with it).
+// memset that atomics want before them (64 x 5120: 3.4 us, 4.4 us with it).
 constexpr int kOneCluster = 32768;
 
 // NVFP4 tensor scales outside this range would leave the exact range of the
