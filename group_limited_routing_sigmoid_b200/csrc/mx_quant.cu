@@ -27,6 +27,7 @@ constexpr int kThreadsQ = 256;
 constexpr int kChunk = 16;         // elements a lane takes at a time
 constexpr int kAhead = 2;          // chunks a lane loads at once
 constexpr int kCluster = 8;
+constexpr long long kMostElements = 1ll << 60;   // sizes in bytes and chunks stay below 2^63
 // Up to this many chunks one cluster finds the tensor scale, without the
 // memset that atomics want before them (64 x 5120: 3.4 us, 4.4 us with it).
 constexpr int kOneCluster = 32768;
@@ -605,6 +606,7 @@ int check_shape(int format, long long rows, int K, int layout)
     if (rows < 0 || rows > (1LL << 40)) return fail(BEAM_ERR_INVALID_ARG, "rows %lld", rows);
     if (K <= 0 || K % block_of(format) != 0)
         return fail(BEAM_ERR_INVALID_ARG, "K must be a positive multiple of %d, got %d", block_of(format), K);
+    if (rows > kMostElements / K) return fail(BEAM_ERR_INVALID_ARG, "%lld x %d elements are too many", rows, K);
     return BEAM_OK;
 }
 
@@ -628,6 +630,7 @@ int beam_mx_tensor_scale(void *stream, const void *x, int dtype, long long rows,
     using namespace beam;
     using namespace beam::ops;
     if (rows < 0 || rows > (1LL << 40) || K < 1) return fail(BEAM_ERR_INVALID_ARG, "rows must be >= 0 and K >= 1");
+    if (rows > kMostElements / K) return fail(BEAM_ERR_INVALID_ARG, "%lld x %d elements are too many", rows, K);
     if (!dtype_ok(dtype)) return fail(BEAM_ERR_INVALID_ARG, "dtype %d", dtype);
     if (!tensor_scale || !aligned(tensor_scale, 4)) return fail(BEAM_ERR_INVALID_ARG, "tensor_scale is NULL or not aligned");
     if (rows > 0 && (!x || !aligned(x, dtype_size(dtype)))) return fail(BEAM_ERR_INVALID_ARG, "x is NULL or not aligned");

@@ -200,10 +200,10 @@ long long block(int format) { return format == BEAM_NVFP4 ? 16 : 32; }
 
 long long scale_count(int format, long long rows, long long K, int layout)
 {
-    if (rows < 0 || K <= 0 || K % block(format)) {
+    if (rows < 0 || K <= 0 || K % block(format) || rows > (1ll << 60) / K) {
         char text[160];
-        snprintf(text, sizeof(text), "K must be a positive multiple of %lld and rows >= 0, got %lld x %lld", block(format),
-                 rows, K);
+        snprintf(text, sizeof(text), "K must be a positive multiple of %lld, rows >= 0 and both fit memory, got %lld x %lld",
+                 block(format), rows, K);
         raise_beam(BEAM_ERR_INVALID_ARG, text);
     }
     const long long n = K / block(format);
@@ -416,11 +416,12 @@ PyObject *matmul(PyObject *const *a, Py_ssize_t n)
     const int fa = small_integer(a[3]), fw = small_integer(a[7]);
     const int T = small_integer(a[8]), N = small_integer(a[9]), K = small_integer(a[10]), dtype = small_integer(a[11]);
     const at::Tensor &first = tensor(a[0], "a.codes", nullptr);
+    const long long a_scales = scale_count(fa, T, K, BEAM_SCALES_TILED), w_scales = scale_count(fw, N, K, BEAM_SCALES_TILED);
     const uint8_t *ac = flat<uint8_t>(a[0], "a.codes", at::kByte, code_bytes(fa, T, K), nullptr);
-    const uint8_t *as = flat<uint8_t>(a[1], "a.scales", at::kByte, scale_count(fa, T, K, BEAM_SCALES_TILED), &first);
+    const uint8_t *as = flat<uint8_t>(a[1], "a.scales", at::kByte, a_scales, &first);
     const float *ag = flat_or_null<float>(a[2], "a.tensor_scale", at::kFloat, 1, &first);
     const uint8_t *wc = flat<uint8_t>(a[4], "w.codes", at::kByte, code_bytes(fw, N, K), &first);
-    const uint8_t *ws = flat<uint8_t>(a[5], "w.scales", at::kByte, scale_count(fw, N, K, BEAM_SCALES_TILED), &first);
+    const uint8_t *ws = flat<uint8_t>(a[5], "w.scales", at::kByte, w_scales, &first);
     const float *wg = flat_or_null<float>(a[6], "w.tensor_scale", at::kFloat, 1, &first);
     const On on(first);
     Rows o;

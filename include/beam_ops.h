@@ -51,7 +51,7 @@ typedef enum { BEAM_NVFP4 = 0, BEAM_MXFP4 = 1, BEAM_MXFP8 = 2 } beam_mx_format;
 typedef enum { BEAM_SCALES_ROWS = 0, BEAM_SCALES_TILED = 1 } beam_scale_layout;
 
 /* Bytes of the scales of a [rows, K] operand, or a negative beam_status.
- * K must be a positive multiple of the format's block. */
+ * K must be a positive multiple of the format's block, rows * K at most 2^60. */
 long long beam_mx_scale_bytes(int format, long long rows, int K, int layout);
 
 /*
@@ -173,8 +173,8 @@ int beam_route_scores(void *stream, const float *logits, int T, int E, long long
 /*
  * Synchronise `stream`, then return and clear the current device's status
  * word of these operators: BEAM_OK, or BEAM_ERR_TIMEOUT when a bounded wait
- * inside beam_mx_matmul ran out since the last call (its result is then not
- * valid).
+ * inside beam_mx_matmul ran out since the last call.  The result of that
+ * product, and of those that ran after it before this call, is not valid.
  */
 int beam_ops_status(void *stream);
 

@@ -714,3 +714,58 @@ def test_product_of_middling_sizes(af, wf, T, N, K):
     check_product(y, torch.float32, av, wv, K)
     assert torch.equal(out[:T, :N], y.half())
     assert (out[T] == 7.0).all() and (out[:, N:] == 7.0).all()
+
+
+def test_operands_of_impossible_sizes_are_refused():
+    e = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for rows, K in ((1 << 40, 1 << 24), (1 << 34, 1 << 30), (-1, 64), (4, 0)):
+        with pytest.raises(ops.BeamMoEError):
+            ops.mx_dequantize(ops.MxTensor(e, e, "mxfp4", "rows", rows, K))
+        with pytest.raises((ops.BeamMoEError, ValueError)):
+            ops.mx_tile_scales(ops.MxTensor(e, e, "mxfp4", "rows", rows, K))
+    t = ops.mx_quantize(rand(4, 128, torch.bfloat16, 0), "mxfp4", "tiled")
+    with pytest.raises((TypeError, ValueError)):
+        ops.mx_matmul(t._replace(rows=1 << 40), t)
+    with pytest.raises(TypeError):
+        ops.mx_matmul(t._replace(rows=5), t)           # not the codes' size
+    with pytest.raises(ops.BeamMoEError):
+        ops.mx_matmul(t._replace(codes=torch.empty(257, dtype=torch.uint8, device="cuda")[1:]), t)   # 32-byte alignment
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+def test_empty_operands(fmt):
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    for layout in ("rows", "tiled"):
+        q = ops.mx_quantize(x, fmt, layout)
+        assert q.rows == 0 and q.scales.numel() == 0 and ops.mx_dequantize(q).shape == (0, 128)
+    a, w = (ops.mx_tile_scales(ops.mx_quantize(t, fmt)) for t in (x, rand(70, 128, torch.bfloat16, 1)))
+    assert ops.mx_matmul(a, w).shape == (0, 70) and ops.mx_matmul(w, a).shape == (70, 0)
+    n = ops.rms_norm(x, torch.ones(128, device="cuda"), residual=x, quantize="mxfp8")
+    assert n.out.shape == n.residual.shape == (0, 128) and n.quantized.rows == 0
+    idx, w = ops.route_scores(torch.empty(0, 8, device="cuda"), 2)
+    assert idx.shape == w.shape == (0, 2)
+
+
+@pytest.mark.parametrize("T,H", [(70, 512), (300, 1000)])
+def test_offset_views_give_the_same(T, H):
+    """Contiguous tensors that start off their allocation's alignment: the same bits, but for the norm, whose squares are
+    summed in the order of its vectors (within check_norm's bound of the exact sum either way)."""
+    b = torch.randn(T * H + 8, generator=torch.Generator().manual_seed(1)).cuda()
+    gamma = torch.ones(H + 8, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        base = b.to(dt)
+        for off in (1, 4, 8):
+            v = base[off:off + T * H].view(T, H)
+            a = v.clone()
+            for t, g in ((v, gamma[off:off + H]), (a, gamma[:H])):
+                check_norm(t, None, g, torch.bfloat16, None, "rows")
+            if H % 32 == 0:
+                for fmt in ("nvfp4", "mxfp4", "mxfp8"):
+                    for layout in ("rows", "tiled"):
+                        p, q = ops.mx_quantize(v, fmt, layout), ops.mx_quantize(a, fmt, layout)
+                        assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+                        out = torch.empty(T * H + 8, dtype=dt, device="cuda")[off:off + T * H].view(T, H)
+                        assert torch.equal(ops.mx_dequantize(q, dt, out), ops.mx_dequantize(q, dt))
+            if dt == torch.float32:
+                i, j = (ops.route_scores(t, 8, score="softmax") for t in (v[:, :512], a[:, :512]))
+                assert torch.equal(i[0], j[0]) and torch.equal(i[1], j[1])

@@ -85,6 +85,15 @@ def test_scale_bytes(lib):
         assert lib.beam_mx_scale_bytes(*bad) == INVALID
 
 
+def test_sizes_past_memory_are_refused(lib):
+    """Products of sizes that wrap around in 64 bits do not pass for small tensors."""
+    assert lib.beam_mx_scale_bytes(1, 1 << 40, 1 << 30, 0) == INVALID
+    assert lib.beam_mx_quantize(None, P(32), 0, 1 << 40, 1 << 30, 1 << 30, 1, 0, None, P(32), P(32)) == INVALID
+    assert lib.beam_mx_dequantize(None, P(32), P(32), None, 1, 0, 1 << 40, 1 << 30, P(32), 0, 1 << 30) == INVALID
+    assert lib.beam_mx_tile_scales(None, 1, P(32), 1 << 40, 1 << 30, P(32)) == INVALID
+    assert lib.beam_mx_tensor_scale(None, P(32), 0, 1 << 40, 1 << 30, 1 << 30, P(32)) == INVALID
+
+
 def quantize(lib, x=16, dtype=0, rows=4, K=64, ldx=64, fmt=1, layout=0, g=None, codes=16, scales=16):
     return lib.beam_mx_quantize(None, x and P(x), dtype, rows, K, ldx, fmt, layout, g and P(g), codes and P(codes),
                                 scales and P(scales))
