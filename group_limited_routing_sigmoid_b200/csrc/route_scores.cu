@@ -147,44 +147,46 @@ __device__ __noinline__ void decide_row(const RouteArgs &p, long long row)
         }
         kept = rank < p.keep;
     }
-    // without a bias the logits order the scores, also where those saturate
+    // Keys as integers that order as they do, 0: not eligible; a round's
+    // largest is found in two halves and the lowest index in a third step.
+    // Without a bias the logits order the scores, also where those saturate.
+    unsigned long long ord[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        if (!kept) key[i] = -INFINITY;
-        if (!BIAS && key[i] > -INFINITY) key[i] = l[my.e0 + i];
+        ord[i] = 0;
+        if (kept && key[i] > -INFINITY) {
+            const long long v = __double_as_longlong(BIAS ? key[i] + 0.0 : (double)l[my.e0 + i] + 0.0);   // -0 as 0
+            ord[i] = (unsigned long long)(v < 0 ? ~v : v ^ (1ll << 63));
+        }
     }
     int my_idx = -1;
     for (int j = 0; j < p.top_k; ++j) {
-        double best = -INFINITY;
+        unsigned long long m = 0;
         int at = p.E;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) best = key[i], at = my.e0 + i;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const double o = __shfl_xor_sync(0xffffffffu, best, d);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, d);
-            if (o > best || (o == best && oa < at)) best = o, at = oa;
-        }
-        if (at == p.E) break;
+            if (ord[i] > m) m = ord[i], at = my.e0 + i;
+        const uint32_t hi = (uint32_t)(m >> 32), best = __reduce_max_sync(0xffffffffu, hi);
+        if (best == 0u) break;
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == best ? (uint32_t)m : 0u);
+        at = (int)__reduce_min_sync(0xffffffffu, hi == best && (uint32_t)m == lo ? (uint32_t)at : 0x7fffffffu);
         if (lane == j) my_idx = at;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (my.e0 + i == at) key[i] = -INFINITY;
+            if (my.e0 + i == at) ord[i] = 0;
     }
-    // weights from the logarithms, so that scores that underflow still share
-    double my_log = -INFINITY;
-    if (my_idx >= 0) {
-        const double x = l[my_idx];
-        my_log = SOFTMAX ? x - top - log(sum) : (x < 0 ? x - log1p(exp(x)) : -log1p(exp(-x)));
-    }
-    double w = my_idx >= 0 ? exp(my_log) : 0.0;
+    const double x = my_idx >= 0 ? (double)l[my_idx] : 0.0;
+    double w = my_idx < 0 ? 0.0 : SOFTMAX ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
     if (p.renorm) {
-        double m = my_log;
+        double s = warp_sum(w);
+        if (s < 1e-200) {   // scores that underflow still share: from their logarithms
+            const double log_w = my_idx < 0 ? -INFINITY : SOFTMAX ? x - top : x < 0 ? x - log1p(exp(x)) : -log1p(exp(-x));
+            double most = log_w;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, d));
-        w = my_idx >= 0 ? exp(my_log - m) : 0.0;
-        const double s = warp_sum(w);
+            for (int d = 16; d; d >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, d));
+            w = my_idx >= 0 ? exp(log_w - most) : 0.0;
+            s = warp_sum(w);
+        }
         w = s > 0.0 ? w / s : 0.0;
     }
     if (lane < p.top_k) {
