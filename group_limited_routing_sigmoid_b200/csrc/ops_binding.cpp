@@ -236,6 +236,45 @@ Operand new_operand(PyObject *codes, PyObject *scales, int format, int layout, l
     return o;
 }
 
+// The fields of an MxTensor, format and layout as the library's codes.
+struct Fields {
+    PyObject *codes, *scales, *tensor_scale;
+    int format, layout;
+    long long rows, K;
+};
+
+int choice(PyObject *o, const char *name, std::initializer_list<const char *> names)
+{
+    int i = 0;
+    if (PyUnicode_Check(o))
+        for (const char *n : names) {
+            if (PyUnicode_CompareWithASCIIString(o, n) == 0) return i;
+            ++i;
+        }
+    std::string all;
+    for (const char *n : names) all += std::string(all.empty() ? "" : ", ") + n;
+    PyErr_Format(PyExc_ValueError, "%s: expected one of %s, got %R", name, all.c_str(), o);
+    throw Raised{};
+}
+
+Fields fields(PyObject *o, const char *name)
+{
+    if (!PyObject_TypeCheck(o, mx_tensor) || PyTuple_GET_SIZE(o) != 7)
+        raise_type("%s: expected an MxTensor, got %s", name, Py_TYPE(o)->tp_name);
+    PyObject **f = &PyTuple_GET_ITEM(o, 0);
+    return {f[0], f[1], f[6], choice(f[2], name, {"nvfp4", "mxfp4", "mxfp8"}), choice(f[3], name, {"rows", "tiled"}),
+            integer(f[4]), integer(f[5])};
+}
+
+int fits(long long v, const char *name)
+{
+    if (v < INT_MIN || v > INT_MAX) {
+        PyErr_Format(PyExc_ValueError, "%s: a size is out of range", name);
+        throw Raised{};
+    }
+    return (int)v;
+}
+
 PyObject *wrap_or_none(const at::Tensor &t)
 {
     if (!t.defined()) Py_RETURN_NONE;
@@ -375,22 +414,21 @@ PyObject *quantize(PyObject *const *a, Py_ssize_t n)
     return pack_operand(q, a[6], a[7], r.rows, r.cols, scale);
 }
 
-// codes, scales, tensor_scale, format, layout, rows, K, dtype, out -> out
+// MxTensor, dtype, out -> out
 PyObject *dequantize(PyObject *const *a, Py_ssize_t n)
 {
-    need(n, 9);
-    const int format = small_integer(a[3]), layout = small_integer(a[4]), dtype = small_integer(a[7]);
-    const long long rows = integer(a[5]);
-    const int K = small_integer(a[6]);
-    const at::Tensor &codes = tensor(a[0], "codes", nullptr);
-    const long long ns = scale_count(format, rows, K, layout);
-    const uint8_t *c = flat<uint8_t>(a[0], "codes", at::kByte, code_bytes(format, rows, K), nullptr);
-    const uint8_t *s = flat<uint8_t>(a[1], "scales", at::kByte, ns, &codes);
-    const float *g = flat_or_null<float>(a[2], "tensor_scale", at::kFloat, 1, &codes);
+    need(n, 3);
+    const Fields q = fields(a[0], "q");
+    const int K = fits(q.K, "q"), dtype = small_integer(a[1]);
+    const at::Tensor &codes = tensor(q.codes, "codes", nullptr);
+    const long long ns = scale_count(q.format, q.rows, K, q.layout);
+    const uint8_t *c = flat<uint8_t>(q.codes, "codes", at::kByte, code_bytes(q.format, q.rows, K), nullptr);
+    const uint8_t *s = flat<uint8_t>(q.scales, "scales", at::kByte, ns, &codes);
+    const float *g = flat_or_null<float>(q.tensor_scale, "tensor_scale", at::kFloat, 1, &codes);
     const On on(codes);
     Rows o;
-    at::Tensor out = output(a[8], "out", rows, K, dtype, codes, o);
-    check(lib.dequantize(on.stream, c, s, g, format, layout, rows, K, o.p, dtype, o.ld));
+    at::Tensor out = output(a[2], "out", q.rows, K, dtype, codes, o);
+    check(lib.dequantize(on.stream, c, s, g, q.format, q.layout, q.rows, K, o.p, dtype, o.ld));
     return THPVariable_Wrap(out);
 }
 
@@ -409,24 +447,32 @@ PyObject *tile_scales(PyObject *const *a, Py_ssize_t n)
     return THPVariable_Wrap(out);
 }
 
-// codes, scales, tensor_scale, format of a; the same of w; T, N, K, dtype, out -> out
+// MxTensor a, MxTensor w, dtype, out -> out
 PyObject *matmul(PyObject *const *a, Py_ssize_t n)
 {
-    need(n, 13);
-    const int fa = small_integer(a[3]), fw = small_integer(a[7]);
-    const int T = small_integer(a[8]), N = small_integer(a[9]), K = small_integer(a[10]), dtype = small_integer(a[11]);
-    const at::Tensor &first = tensor(a[0], "a.codes", nullptr);
-    const long long a_scales = scale_count(fa, T, K, BEAM_SCALES_TILED), w_scales = scale_count(fw, N, K, BEAM_SCALES_TILED);
-    const uint8_t *ac = flat<uint8_t>(a[0], "a.codes", at::kByte, code_bytes(fa, T, K), nullptr);
-    const uint8_t *as = flat<uint8_t>(a[1], "a.scales", at::kByte, a_scales, &first);
-    const float *ag = flat_or_null<float>(a[2], "a.tensor_scale", at::kFloat, 1, &first);
-    const uint8_t *wc = flat<uint8_t>(a[4], "w.codes", at::kByte, code_bytes(fw, N, K), &first);
-    const uint8_t *ws = flat<uint8_t>(a[5], "w.scales", at::kByte, w_scales, &first);
-    const float *wg = flat_or_null<float>(a[6], "w.tensor_scale", at::kFloat, 1, &first);
+    need(n, 4);
+    const Fields x = fields(a[0], "a"), w = fields(a[1], "w");
+    if (x.layout != BEAM_SCALES_TILED || w.layout != BEAM_SCALES_TILED) {
+        PyErr_SetString(PyExc_ValueError, "mx_matmul takes scales in the tiled layout (mx_tile_scales)");
+        throw Raised{};
+    }
+    if (x.K != w.K) {
+        PyErr_Format(PyExc_ValueError, "a has %lld columns, w %lld", x.K, w.K);
+        throw Raised{};
+    }
+    const int T = fits(x.rows, "a"), N = fits(w.rows, "w"), K = fits(x.K, "a"), dtype = small_integer(a[2]);
+    const at::Tensor &first = tensor(x.codes, "a.codes", nullptr);
+    const long long x_scales = scale_count(x.format, T, K, BEAM_SCALES_TILED), w_scales = scale_count(w.format, N, K, BEAM_SCALES_TILED);
+    const uint8_t *xc = flat<uint8_t>(x.codes, "a.codes", at::kByte, code_bytes(x.format, T, K), nullptr);
+    const uint8_t *xs = flat<uint8_t>(x.scales, "a.scales", at::kByte, x_scales, &first);
+    const float *xg = flat_or_null<float>(x.tensor_scale, "a.tensor_scale", at::kFloat, 1, &first);
+    const uint8_t *wc = flat<uint8_t>(w.codes, "w.codes", at::kByte, code_bytes(w.format, N, K), &first);
+    const uint8_t *ws = flat<uint8_t>(w.scales, "w.scales", at::kByte, w_scales, &first);
+    const float *wg = flat_or_null<float>(w.tensor_scale, "w.tensor_scale", at::kFloat, 1, &first);
     const On on(first);
     Rows o;
-    at::Tensor out = output(a[12], "out", T, N, dtype, first, o);
-    check(lib.matmul(on.stream, fa, ac, as, ag, fw, wc, ws, wg, T, N, K, o.p, dtype, o.ld));
+    at::Tensor out = output(a[3], "out", T, N, dtype, first, o);
+    check(lib.matmul(on.stream, x.format, xc, xs, xg, w.format, wc, ws, wg, T, N, K, o.p, dtype, o.ld));
     return THPVariable_Wrap(out);
 }
 

@@ -86,9 +86,10 @@ def _native():
 
 def _elsewhere(stream, f, *args):
     """f(*args) on `stream` of the first argument's device, all tensors marked as used there."""
-    if not isinstance(args[0], torch.Tensor) or not args[0].is_cuda:
+    first = args[0].codes if isinstance(args[0], MxTensor) else args[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
         return f(*args)                # which refuses it
-    device = args[0].device
+    device = first.device
     if isinstance(stream, torch.cuda.Stream) and stream.device != device:
         raise ValueError(f"stream on {stream.device}, tensors on {device}")
     with torch.cuda.device(device):
@@ -176,9 +177,9 @@ def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale
 
 def mx_dequantize(q: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of a microscaled operand, [rows, K]."""
-    args = (*_operand(q, "q"), _key(DTYPES, dtype, "dtype"), out)
+    d = _key(DTYPES, dtype, "dtype")
     f = (_binding or _native()).dequantize
-    return f(*args) if stream is None else _elsewhere(stream, f, *args)
+    return f(q, d, out) if stream is None else _elsewhere(stream, f, q, d, out)
 
 
 def mx_tile_scales(q: MxTensor, stream=None) -> MxTensor:
@@ -194,16 +195,9 @@ def mx_tile_scales(q: MxTensor, stream=None) -> MxTensor:
 def mx_matmul(a: MxTensor, w: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
     """a [T, K] . w [N, K]^T -> [T, N]: NVFP4 x NVFP4, MXFP4 x MXFP4, MXFP8 x MXFP4 or MXFP8 x MXFP8, scales tiled."""
-    ac, asc, ag, af, al, T, K = _operand(a, "a")
-    wc, wsc, wg, wf, wl, N, wk = _operand(w, "w")
-    if al != 1 or wl != 1:
-        raise ValueError("mx_matmul takes scales in the tiled layout (mx_tile_scales)")
-    if K != wk:
-        raise ValueError(f"a has {K} columns, w {wk}")
-    f = (_binding or _native()).matmul
     d = _key(DTYPES, dtype, "dtype")
-    return (f(ac, asc, ag, af, wc, wsc, wg, wf, T, N, K, d, out) if stream is None else
-            _elsewhere(stream, f, ac, asc, ag, af, wc, wsc, wg, wf, T, N, K, d, out))
+    f = (_binding or _native()).matmul
+    return f(a, w, d, out) if stream is None else _elsewhere(stream, f, a, w, d, out)
 
 
 # --- norm and routing ----------------------------------------------------------

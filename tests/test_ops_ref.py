@@ -218,13 +218,22 @@ def test_binding_turns_refusals_into_exceptions():
     """The compiled binding's own checks: what is no tensor, wrong counts, integers and reals out of place."""
     f = ops._native()
     x = torch.zeros(4, 64)
+    q = ops.MxTensor(x, x, "mxfp4", "rows", 4, 64)
     for call, args in ((f.quantize, (x, 1)), (f.quantize, (3, 1, 0, None, None, None, "mxfp4", "rows")),
                        (f.quantize, (None,) * 8),
-                       (f.rms_norm, (x,) * 15), (f.matmul, ("a",) * 13), (f.dequantize, (x, x, None, 1, 0, 4, "K", 0, None)),
+                       (f.rms_norm, (x,) * 15), (f.matmul, ("a",) * 4), (f.matmul, (x, x, 0, None)),
+                       (f.dequantize, ((x, x, "mxfp4", "rows", 4, 64, None), 0, None)), (f.dequantize, (q, 0, None)),
+                       (f.dequantize, (q._replace(K="K"), 0, None)), (f.matmul, (q._replace(layout="tiled"),) * 2 + (0, None)),
                        (f.tile_scales, (x, 1, 2.5, 64)), (f.route_scores, (x,) * 11), (f.tensor_scale, (x, None))):
         with pytest.raises(TypeError):
             call(*args)
     with pytest.raises(ValueError):
         f.tile_scales(x, 1 << 40, 4, 64)
+    for call, args in ((f.dequantize, (q._replace(format="fp4"), 0, None)), (f.dequantize, (q._replace(layout=1), 0, None)),
+                       (f.dequantize, (q._replace(K=1 << 40), 0, None)), (f.matmul, (q, q, 0, None)),
+                       (f.matmul, (q._replace(layout="tiled"), q._replace(layout="tiled", K=32), 0, None)),
+                       (f.matmul, (q._replace(layout="tiled", rows=1 << 33),) * 2 + (0, None))):
+        with pytest.raises(ValueError):
+            call(*args)
     with pytest.raises(OverflowError):
         f.tile_scales(x, 1, 1 << 80, 64)
