@@ -77,17 +77,20 @@ struct Span {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The approximations below flush subnormals (3 instructions less each): what
+// they are used for is compared with margins far above 2^-126.
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
 __device__ __forceinline__ float rcp_fast(float x)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -297,8 +300,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
             }
             float pa = a, pb = b;
             if constexpr (!BIAS) {   // softmax: up to the common factor
-                pa = a > -INFINITY ? (SOFTMAX ? expf(a - top) : sigmoid(a)) : -INFINITY;
-                pb = b > -INFINITY ? (SOFTMAX ? expf(b - top) : sigmoid(b)) : -INFINITY;
+                pa = a > -INFINITY ? (SOFTMAX ? exp2_fast((a - top) * kLog2e) : sigmoid_fast(a)) : -INFINITY;
+                pb = b > -INFINITY ? (SOFTMAX ? exp2_fast((b - top) * kLog2e) : sigmoid_fast(b)) : -INFINITY;
             }
             const float score = p.group_top == 2 && pb > -INFINITY ? pa + pb : pa;
             float left = score, lo = -INFINITY;
@@ -414,13 +417,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
             const bool outside = check && lane == p.top_k - 1 && !(k0 - bound > tol);
             const bool near = check && lane + 1 < n && !(k0 - k1 > tol) &&
                               !(lane + 1 < p.top_k && tie[lane].x == tie[lane + 1].x && tie[lane].y == tie[lane + 1].y);
-            if (__any_sync(0xffffffffu, outside || (SOFTMAX && near))) {
+            if (__any_sync(0xffffffffu, outside)) {
                 decide_row<EPL, SOFTMAX, BIAS>(p, row);
                 continue;
             }
-            if (!SOFTMAX && __any_sync(0xffffffffu, near)) {
+            if (__any_sync(0xffffffffu, near)) {
                 // all that may be chosen are candidates: rank those in 64 bits
-                const double exact = in ? 1.0 / (1.0 + exp(-(double)xe)) + (double)be : -INFINITY;
+                double total = 1.0;
+                if constexpr (SOFTMAX) {
+                    double part = 0.0;
+#pragma unroll 1
+                    for (int i = 0; i < my.mine; ++i) part += exp((double)l[my.e0 + i] - (double)top);
+                    total = warp_sum(part);
+                }
+                const double exact = in ? (SOFTMAX ? exp((double)xe - (double)top) / total : 1.0 / (1.0 + exp(-(double)xe))) + (double)be
+                                        : -INFINITY;
                 rank = 0;
                 for (int m = 0; m < n; ++m) {
                     const double o = __shfl_sync(0xffffffffu, exact, m);
