@@ -20,7 +20,7 @@ struct NormArgs {
     void *out;
     uint8_t *codes, *scales;
     long long ldx, ldr, ldro, ldo;
-    int T, H, out_dtype;
+    int T, H, out_dtype, gamma_vec;   // gamma_vec: gamma starts on 16 bytes
     float alpha, beta, eps;
     ScaleMap map;
 };
@@ -175,13 +175,12 @@ __global__ void __launch_bounds__(WARP_ROWS ? 128 : NV == 2 ? 512 : 1024,
     RT *ro = HAS_R ? static_cast<RT *>(p.ro) + (size_t)row * p.ldro : nullptr;
     float g[EARLY ? NV : 1][8];
     const auto load_gamma = [&](int e, float (&v)[8]) {
-        if constexpr (ALIGNED) {
+        if (ALIGNED || (p.gamma_vec && e + 8 <= p.H)) {
             const float4 a = *reinterpret_cast<const float4 *>(p.gamma + e), b = *reinterpret_cast<const float4 *>(p.gamma + e + 4);
             v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
-            uint32_t o;
-            const Units<float> u = load_units(p.gamma, e, p.H, p.gamma, p.gamma + p.H, o);
-            unpack8(shift_units(u, o), v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = e + q < p.H ? p.gamma[e + q] : 0.f;
         }
     };
     if constexpr (ALIGNED) {
@@ -378,7 +377,7 @@ extern "C" int beam_rms_norm(void *stream, const void *x, int x_dtype, long long
                      (!residual || (rows_aligned16(residual, ldr, residual_dtype) &&
                                     rows_aligned16(residual_out, ldro, residual_dtype))) &&
                      (!out || rows_aligned16(out, ldo, out_dtype));
-    NormArgs a{x, residual, residual_out, gamma, out, codes, scales, ldx, ldr, ldro, ldo, T, H, out_dtype,
+    NormArgs a{x, residual, residual_out, gamma, out, codes, scales, ldx, ldr, ldro, ldo, T, H, out_dtype, aligned(gamma, 16),
                alpha, beta, eps, ScaleMap(codes ? layout : 0, H / 32)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
