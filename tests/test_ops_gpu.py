@@ -769,3 +769,25 @@ def test_offset_views_give_the_same(T, H):
             if dt == torch.float32:
                 i, j = (ops.route_scores(t, 8, score="softmax") for t in (v[:, :512], a[:, :512]))
                 assert torch.equal(i[0], j[0]) and torch.equal(i[1], j[1])
+
+
+@pytest.mark.parametrize("af,wf", PAIRS)
+@pytest.mark.parametrize("T,N,K", [(1, 18945, 128), (3, 18960, 256), (16, 19000, 640), (33, 20480, 384), (64, 20480, 1152),
+                                   (64, 21313, 256), (20, 23680, 256), (64, 23681, 128)])
+def test_product_a_few_tiles_more_than_sms(af, wf, T, N, K):
+    """One to 37 weight tiles more than one for every SM; whole numbers, exact in any order."""
+    rng = np.random.default_rng(N)
+    opnds, vals = [], []
+    for rows, fmt in ((T, af), (N, wf)):
+        e = rng.integers(0, 3, (rows, K)).astype(float) * rng.choice([-1.0, 1.0], (rows, K))
+        one = 0x38 if fmt == "nvfp4" else 127
+        up = rng.integers(0, 2, (rows, K // R.BLOCK[fmt]))
+        sb = (one + up * (8 if fmt == "nvfp4" else 1)).astype(np.uint8)
+        opnds.append(ops.MxTensor(torch.from_numpy(R.codes(e, fmt)).cuda(), torch.from_numpy(R.tile(sb)).cuda(), fmt, "tiled", rows, K))
+        vals.append(R.values(e, sb, fmt))
+    want = vals[0] @ vals[1].T
+    out = torch.full((T + 1, N + 5), 7.0, dtype=torch.float32, device="cuda")
+    ops.mx_matmul(*opnds, torch.float32, out=out[:T, :N])
+    assert ops.ops_status() == 0
+    np.testing.assert_array_equal(f64(out[:T, :N]), want)
+    assert (out[T] == 7.0).all() and (out[:, N:] == 7.0).all()
