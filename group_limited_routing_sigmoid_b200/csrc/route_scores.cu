@@ -6,8 +6,8 @@
 // experts whose key reaches the n-th largest of the lanes' best keys (n the
 // experts wanted) hold the n largest and are few (about 13 of 256 for n = 9).
 // They are packed, one to a lane, and ranked by counting the larger ones.
-// 32768 x 256, 8 groups of which 4 stay, bias, top 8: 34 us (1.06 TB/s); without
-// groups and bias 22 us.  Lists sorted in the lanes with one maximum over their
+// 32768 x 256, 8 groups of which 4 stay, bias, top 8: 33 us (1.07 TB/s); without
+// groups and bias 21 us.  Lists sorted in the lanes with one maximum over their
 // heads per expert wanted took 49 and 26 us.
 //
 // Decisions are those of exact arithmetic: an FP32 score is off by a few
@@ -518,7 +518,7 @@ extern "C" int beam_route_scores(void *stream, const float *logits, int T, int E
     if (a.epl > 2) a.epl = (a.epl + 3) / 4 * 4;   // whole 16-byte loads
     a.vec = a.size % 4 == 0 && a.epl % 4 == 0 && rows_aligned16(logits, ldl, BEAM_F32);
     // twice the resident blocks: the second half starts where rows decided in
-    // 64 bits leave room (34 us; 38 with resident blocks only)
+    // 64 bits leave room (when measured, 34 us; 38 with resident blocks only)
     const long long need = ((long long)T + kRouteWarps - 1) / kRouteWarps;
     const dim3 grid((unsigned)(need < 8LL * sms ? need : 8LL * sms));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
