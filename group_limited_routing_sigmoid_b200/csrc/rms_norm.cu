@@ -364,6 +364,7 @@ extern "C" int beam_rms_norm(void *stream, const void *x, int x_dtype, long long
     if (codes && H % 32 != 0) return fail(BEAM_ERR_INVALID_ARG, "H must be a multiple of 32 for MXFP8, got %d", H);
     if (!(eps >= 0.f) || !(alpha - alpha == 0.f) || !(beta - beta == 0.f))
         return fail(BEAM_ERR_INVALID_ARG, "eps must be >= 0, alpha and beta finite");
+    if (T > 0x7fffff00) return fail(BEAM_ERR_UNSUPPORTED, "T must be at most 2^31 - 256, got %d", T);
     if (H > 32768) return fail(BEAM_ERR_UNSUPPORTED, "H must be at most 32768, got %d", H);
     if (T == 0) return BEAM_OK;
     if (!x || !gamma || (!out && !codes)) return fail(BEAM_ERR_INVALID_ARG, "x, gamma and an output are required");

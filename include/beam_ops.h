@@ -136,7 +136,8 @@ int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes, const uin
  * codes, scales  MXFP8 of y (from FP32, not from the rounded out), as
  *              beam_mx_quantize writes them, in `layout`; both or neither.
  *              H must be a multiple of 32 then.
- * 1 <= H <= 32768 (else BEAM_ERR_UNSUPPORTED), T >= 0 (0: nothing to do).
+ * 1 <= H <= 32768 and T <= 2^31 - 256 (else BEAM_ERR_UNSUPPORTED), T >= 0 (0:
+ * nothing to do).
  */
 int beam_rms_norm(void *stream, const void *x, int x_dtype, long long ldx, const void *residual,
                   int residual_dtype, long long ldr, void *residual_out, long long ldro,

@@ -791,3 +791,68 @@ def test_product_a_few_tiles_more_than_sms(af, wf, T, N, K):
     assert ops.ops_status() == 0
     np.testing.assert_array_equal(f64(out[:T, :N]), want)
     assert (out[T] == 7.0).all() and (out[:, N:] == 7.0).all()
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every operator is captured: nothing that loads on first use may break the capture."""
+    import os
+    import subprocess
+    import sys
+    import textwrap
+
+    code = textwrap.dedent("""
+        import torch
+        from group_limited_routing_sigmoid_b200 import ops
+        T, H = 70, 512
+        x = torch.randn(T, H, device="cuda").bfloat16()
+        r, gamma, l = torch.randn(T, H, device="cuda"), torch.ones(H, device="cuda"), torch.randn(T, 60, device="cuda")
+        wide = torch.randn(600, H, device="cuda").bfloat16()
+        torch.cuda.synchronize()
+        def run():
+            n = ops.rms_norm(x, gamma, residual=r, quantize="mxfp8")
+            w = ops.mx_tile_scales(ops.mx_quantize(wide, "mxfp4"))
+            y = ops.mx_matmul(n.quantized, w)
+            q = ops.mx_quantize(wide, "nvfp4", "tiled")
+            return [n.out, y, ops.mx_matmul(q, q), ops.mx_dequantize(q), *ops.route_scores(l, 4, score="softmax")]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, run()))
+        assert ops.ops_status() == 0
+    """)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_two_threads_at_once():
+    """Calls of several threads, each on its own stream, one of them refused: results and error texts are the thread's own."""
+    import threading
+
+    args = [run_inputs(s) for s in (0, 50, 90)]
+    want = [run_all(*a) for a in args]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.default_stream())
+            for _ in range(20):
+                got = run_all(*args[i], stream=s)
+                with pytest.raises(ops.BeamMoEError, match="top_k"):
+                    ops.route_scores(args[i][4], 61 + i)
+            s.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                bad.append(i)
+        except BaseException as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and ops.ops_status() == 0

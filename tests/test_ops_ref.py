@@ -170,7 +170,7 @@ def norm(lib, x=16, xd=0, ldx=64, r=None, rd=0, ldr=64, ro=None, ldro=64, alpha=
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), INVALID), (dict(gamma=None), INVALID), (dict(out=None), INVALID), (dict(T=-1), INVALID),
-    (dict(H=0), INVALID), (dict(H=32769, ldx=32769, ldo=32769), UNSUPPORTED), (dict(xd=3), INVALID),
+    (dict(H=0), INVALID), (dict(T=2 ** 31 - 1), UNSUPPORTED), (dict(H=32769, ldx=32769, ldo=32769), UNSUPPORTED), (dict(xd=3), INVALID),
     (dict(od=3), INVALID), (dict(r=16), INVALID), (dict(ro=16), INVALID), (dict(r=16, ro=32, rd=1), INVALID),
     (dict(ldx=63), INVALID), (dict(ldo=63), INVALID), (dict(r=16, ro=32, rd=2, ldr=60), INVALID),
     (dict(codes=16), INVALID), (dict(scales=16), INVALID), (dict(codes=16, scales=16, layout=2), INVALID),
