@@ -18,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -77,8 +78,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     hdr_time = _newest(headers) if headers else 0
-    objs = []
-    rebuilt = False
+    objs, commands = [], []
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -89,9 +89,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
                 cmd += ["-Xptxas", "-v"]
             if not quiet:
                 print(" ".join(cmd), flush=True)
-            subprocess.check_call(cmd)
-            rebuilt = True
-    if rebuilt or force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
+            commands.append(cmd)
+    with ThreadPoolExecutor(max(1, os.cpu_count() or 1)) as pool:   # the sources are independent
+        list(pool.map(subprocess.check_call, commands))
+    if commands or force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
         if not quiet:
