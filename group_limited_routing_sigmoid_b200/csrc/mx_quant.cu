@@ -330,6 +330,9 @@ template <typename T, bool ONE, int AL>
 __global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, float *out)
 {
     constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;
+    // every block of the cluster has started before one writes into another's
+    // shared memory (waited for below, when the data has been read)
+    if constexpr (ONE) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_launch_dependents();
     pdl_wait();
     const T *x = static_cast<const T *>(p.x);
@@ -383,6 +386,8 @@ __global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, f
     }
     if constexpr (ONE) {
         __shared__ uint32_t all[kCluster];
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (threadIdx.x == 0)
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&all[cluster_ctarank()]), 0)), "r"(m)
                          : "memory");
