@@ -76,7 +76,7 @@ def build_binding(force: bool = False, quiet: bool = False) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     hdr_time = _newest(headers) if headers else 0
     objs, commands = [], []
     for src in sources:

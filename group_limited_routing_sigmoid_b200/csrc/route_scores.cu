@@ -16,9 +16,15 @@
 // exactly equal, is decided again from 64-bit scores (decide_row, the same
 // warp).  Without a bias the keys are the logits themselves, which are exact.
 //
+// A lane owns up to 60 experts where n_group is no power of two (route_layout.h).
+// 4096 x 720, 10 groups of which 4 stay: 17 us, 50 with a bias (sigmoid; 23 and
+// 58 at one block an SM and twice the registers, which only 60 experts a lane
+// gain from: 4096 x 1020, 17 groups, bias 77 and 66 us).
+//
 // Bound by instruction issue at large T, by the latency of a row's chain of
 // warp-wide steps at small T.
 #include "ops_common.cuh"
+#include "route_layout.h"
 
 namespace beam {
 namespace {
@@ -33,9 +39,7 @@ struct RouteArgs {
     float *w;
     long long ldl;
     int T, E;
-    int lanes_log;  // log2 of the lanes a group has (5 when no groups are dropped)
-    int size;       // experts a group (E when no groups are dropped)
-    int epl;        // experts a lane
+    int lanes_log, size, epl;   // RouteLayout
     int keep;       // groups that stay, 0: all
     int group_top, top_k, renorm;
     int vec;        // rows and lanes start on 16-byte boundaries
@@ -64,16 +68,10 @@ __device__ __forceinline__ F warp_sum(F v)
     return v;
 }
 
-// The lane's experts: `mine` of them from e0.
-struct Span {
-    int e0, mine;
-    __device__ __forceinline__ Span(const RouteArgs &p, int lane)
-    {
-        const int sub = (lane & ((1 << p.lanes_log) - 1)) * p.epl, g = lane >> p.lanes_log;
-        e0 = g * p.size + sub;
-        mine = e0 < p.E ? max(min(p.size - sub, p.epl), 0) : 0;
-    }
-};
+__device__ __forceinline__ Span span_of(const RouteArgs &p, int lane)
+{
+    return Span(lane, p.lanes_log, p.size, p.epl, p.E);
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -107,7 +105,7 @@ template <int EPL, bool SOFTMAX, bool BIAS>
 __device__ __noinline__ void decide_row(const RouteArgs &p, long long row)
 {
     const int lane = threadIdx.x & 31;
-    const Span my(p, lane);
+    const Span my = span_of(p, lane);
     const float *l = p.logits + row * p.ldl;
     const int lanes = 1 << p.lanes_log;
     double top = -INFINITY, sum = 1.0;
@@ -210,7 +208,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t below = (1u << lane) - 1u;
-    const Span my(p, lane);
+    const Span my = span_of(p, lane);
     float *cand = s_key[warp];
     int *expert = s_expert[warp];
     // with a bias one more than top_k: the best that is not chosen
@@ -283,11 +281,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
         }
         // How far two FP32 keys may be off together.  Sigmoid: 2^-22 each
         // (s(1-s) times the exponential's 2^-22 and its argument's rounding,
-        // half an ulp of the sum, an ulp of the reciprocal).  Softmax: some
-        // ulps of the largest score 1 / sum each (exponential 2, its
-        // argument's rounding, 37 partial sums, two products).  And the
-        // rounding of the added bias.
-        const float tol_score = SOFTMAX ? 0x1p-19f * rcp_fast(sum) : 0x1p-20f;
+        // half an ulp of the sum, an ulp of the reciprocal).  Softmax, in
+        // units of 2^-24 / sum (the largest score is 1 / sum): the keys' own
+        // exponentials 4 and 1 for its argument, and what both share, the
+        // sum's partial sums EPL + 4 (EPL - 1 in the lane, 5 across), its
+        // exponentials 4, their arguments 10 (3 roundings of the weighted mean
+        // distance from the top, at most 3.4 for 1024 experts), its reciprocal
+        // 2 and a product 1, all times the scores' difference: up to 30 for
+        // 8 experts a lane, 54 for 32, 86 for 64.  And the rounding of the
+        // added bias.
+        constexpr float kSoftmaxTol = EPL <= 8 ? 0x1p-19f : EPL <= 32 ? 0x1p-18f : 0x1p-17f;
+        const float tol_score = SOFTMAX ? kSoftmaxTol * rcp_fast(sum) : 0x1p-20f;
         bool close = false;
         if (p.keep) {
             float a = key[0], b = -INFINITY;
@@ -509,13 +513,9 @@ extern "C" int beam_route_scores(void *stream, const float *logits, int T, int E
     a.logits = logits, a.bias = bias, a.idx = topk_idx, a.w = topk_w;
     a.ldl = ldl, a.T = T, a.E = E;
     a.group_top = group_top, a.top_k = top_k, a.renorm = renormalize != 0, a.scale = scale;
-    const bool groups = topk_group < n_group;
-    a.keep = groups ? topk_group : 0;
-    a.lanes_log = 5;
-    while (groups && n_group << a.lanes_log > 32) --a.lanes_log;
-    a.size = groups ? E / n_group : E;
-    a.epl = (a.size + (1 << a.lanes_log) - 1) >> a.lanes_log;
-    if (a.epl > 2) a.epl = (a.epl + 3) / 4 * 4;   // whole 16-byte loads
+    a.keep = topk_group < n_group ? topk_group : 0;
+    const RouteLayout how = route_layout(E, n_group, topk_group);
+    a.lanes_log = how.lanes_log, a.size = how.size, a.epl = how.epl;
     a.vec = a.size % 4 == 0 && a.epl % 4 == 0 && rows_aligned16(logits, ldl, BEAM_F32);
     // twice the resident blocks: the second half starts where rows decided in
     // 64 bits leave room (when measured, 34 us; 38 with resident blocks only)
@@ -524,11 +524,15 @@ extern "C" int beam_route_scores(void *stream, const float *logits, int T, int E
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool softmax = score == BEAM_SCORE_SOFTMAX;
     cudaError_t e;
-    if (a.epl <= 1) e = launch<1>(a, softmax, grid, s);
-    else if (a.epl <= 2) e = launch<2>(a, softmax, grid, s);
-    else if (a.epl <= 4) e = launch<4>(a, softmax, grid, s);
-    else if (a.epl <= 8) e = launch<8>(a, softmax, grid, s);
-    else if (a.epl <= 16) e = launch<16>(a, softmax, grid, s);
-    else e = launch<32>(a, softmax, grid, s);
+    switch (how.regs) {
+        case 1: e = launch<1>(a, softmax, grid, s); break;
+        case 2: e = launch<2>(a, softmax, grid, s); break;
+        case 4: e = launch<4>(a, softmax, grid, s); break;
+        case 8: e = launch<8>(a, softmax, grid, s); break;
+        case 16: e = launch<16>(a, softmax, grid, s); break;
+        case 32: e = launch<32>(a, softmax, grid, s); break;
+        case 64: e = launch<64>(a, softmax, grid, s); break;
+        default: return fail(BEAM_ERR_UNSUPPORTED, "%d experts in %d groups", E, n_group);
+    }
     return check_cuda(e, "beam_route_scores");
 }

@@ -34,3 +34,51 @@ def test_small_tensor_scales_beside_other_work():
         torch.cuda.synchronize()
         assert [float(t) for t in got] == want
     del busy
+
+
+def check_route(l, k, score, bias=None, G=1, keep=1, gtop=2, renorm=True, scale=1.0):
+    idx, w = ops.route_scores(l, k, score=score, bias=bias, n_group=G, topk_group=keep, group_top=gtop, renormalize=renorm, scale=scale)
+    ri, rw = R.route(f64(l), k, score, None if bias is None else bias.cpu().numpy(), G, keep, gtop, renorm, scale)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    got = f64(w)
+    assert np.array_equal(np.isnan(got), np.isnan(rw))
+    ok = ~np.isnan(rw)
+    # two exponentials of 2 ulps, E / lanes + 5 <= 69 partial sums and two roundings, in units of half an ulp
+    np.testing.assert_allclose(got[ok], rw[ok], rtol=(8 + 69 + 2) * 2.0 ** -24, atol=2.0 ** -149)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep", [(720, 10, 4), (960, 10, 3), (1000, 5, 2), (1017, 9, 8), (561, 17, 1), (1020, 17, 16),
+                                      (1023, 3, 2), (930, 31, 30), (1015, 29, 5), (768, 24, 7), (1020, 20, 19), (510, 30, 2)])
+def test_route_group_counts_that_are_no_power_of_two(score, E, G, keep):
+    """Up to 60 experts a lane; the best ones lie last in their lanes in some rows, NaN and masks too."""
+    g = torch.Generator().manual_seed(E + G)
+    l = torch.randn(40, E, generator=g) * 2
+    size = E // G
+    l[8:16, size - 1::size] += 6.0                     # the last expert of every group
+    l[16:20] = l[16:20].sort(dim=1).values
+    l[20, E - 1] = float("nan")
+    l[21, size - 1] = float("nan")
+    l[22] = -float("inf")
+    l[23, : E - 1] = -float("inf")
+    l[24] = l[24].to(torch.bfloat16).float()
+    l[25] = 0.0
+    l = l.cuda()
+    k = min(8, keep * size)
+    for bias in (None, (torch.randn(E, generator=g) * 0.05).cuda()):
+        for gtop in (1, 2):
+            for renorm in (False, True):
+                check_route(l, k, score, bias, G, keep, gtop, renorm, 2.5)
+
+
+def test_route_sums_that_lose_their_small_terms():
+    """A lane that adds 59 terms of 0.9 x 2^-24 to one keeps none of them in FP32; a key 47 steps of 2^-24 below one comes
+    before the first expert's, 53 below, only in exact arithmetic."""
+    E, G = 1020, 17
+    l = torch.full((4, E), -100.0)
+    l[:, 960:] = -float("inf")                         # the group that is dropped
+    l[:, 0] = 0.0
+    l[:, 1:60] = float(np.log(0.9 * 2.0 ** -24))
+    bias = torch.zeros(E)
+    bias[200], bias[300] = 1 - 47 * 2.0 ** -24, 0.5    # the second: what is not chosen lies far below
+    check_route(l.cuda(), 2, "softmax", bias.cuda(), G, 16, 2, False)
