@@ -477,63 +477,6 @@ cudaError_t launch_bn(int bn, const Maps &m, const MatmulArgs &a, int ctas, cuda
     }
 }
 
-// Clusters of 1 to 8 CTAs that a B200 holds at once, at one and two CTAs an SM
-// (cudaOccupancyMaxActiveClusters with these kernels' threads and shared
-// memory).  More clusters than fit only wait for their turn.
-constexpr int kClusters[2][8] = {{148, 74, 45, 33, 26, 22, 15, 15}, {296, 148, 93, 71, 56, 45, 37, 33}};
-
-struct Plan {
-    int bn, split;
-    bool pair;
-    long long cost;   // ns
-};
-
-// Tile width and split of K with the least estimated time.  The estimate: 2.5
-// us of launch; a tile's set-up and epilogue; its stages one after another (a
-// stage of a lone CTA waits on its loads and scale copies, 0.3 us + 2 ns a
-// column, longer where two CTAs share an SM); the sum over a cluster; and for
-// more tiles than CTAs the waves of them.  It was fitted to tiles of 32 to
-// 128 columns split 1 to 8 times (500 x 500 x 512: 5.0 us at 64 columns, 6.2 at
-// 128; 300 x 1000 x 5120: 9.9 us split 4 ways, 18.3 whole; 1 x 5120 x 20480:
-// 13.5 us split 6 ways, 16.3 four ways, 25 two ways) and pairs (2048 x 5120 x
-// 5120 MXFP8 x MXFP4: 50 us, 70 on single CTAs; 1021 x 5123 x 2560: 20.7 us,
-// 17.5 on single CTAs, whose many tiles hide the odd rows' stores better).
-Plan plan(int kind, int P, int Q, int nst, bool swap, bool vec, int sms)
-{
-    const long long p_tiles = (P + kTileP - 1) / kTileP;
-    Plan best{0, 1, false, 0};
-    const auto offer = [&](int bn, int split, bool pair, long long cost) {
-        if (best.bn == 0 || cost < best.cost) best = Plan{bn, split, pair, cost};
-    };
-    for (int bn = 16; bn <= 128; bn *= 2) {
-        if (bn < 64 && bn < Q) continue;        // one tile of B, or scales at even columns
-        const long long tiles = p_tiles * ((Q + bn - 1) / bn);
-        const int per_sm = bn <= 64 ? 2 : 1;
-        const long long fixed = 900 + 12 * bn;
-        if (tiles > (long long)sms * per_sm) {   // persistent, the epilogue beside the next tile
-            if (bn < 128 && !swap) continue;     // whose stores are then by columns
-            const long long waves = (tiles + sms * per_sm - 1) / (sms * per_sm);
-            offer(bn, 1, false, 2500 + fixed + waves * (nst * 410ll * per_sm + (vec ? 0 : 800)));
-        } else {
-            // clusters that all fit at once
-            for (int s = 1; s <= 8 && s <= nst && tiles <= kClusters[per_sm - 1][s - 1]; ++s) {
-                // CTAs an SM, in thousandths: 8-bit stages mostly wait, 4-bit
-                // ones (twice the K) are held up by the SM's other CTA
-                const int ctas = (int)tiles * s, mean = ctas > sms ? ctas * 1000 / sms : 1000;
-                const int share = kind == kMx8 || mean == 1000 ? mean : (mean + 2000) / 2;
-                const int stage = (300 + 2 * bn) * share / 1000;
-                offer(bn, s, false, 2500 + fixed + (s > 1 ? 300 + 100 * s : 0) + (long long)((nst + s - 1) / s) * stage);
-            }
-        }
-        if (bn >= Q) break;
-    }
-    if (!swap && P > 128 && Q > 128) {
-        const long long tiles = (long long)((P + 255) / 256) * ((Q + 255) / 256), waves = (tiles + sms / 2 - 1) / (sms / 2);
-        offer(256, 1, true, 5000 + waves * (nst * 500ll + (vec ? 0 : 2900)));
-    }
-    return best;
-}
-
 // Device address of the status word, looked up once per device.
 std::atomic<int *> g_status_ptr[64];
 
@@ -601,6 +544,7 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
     a.ksteps = K / step_k(kind);
     const int n4 = (K / block_of(a_format) + 3) / 4;
     const Plan how = plan(kind, a.P, a.Q, a.nst, swap, a.vec != 0, sms);
+    if (how.bn == 0) return fail(BEAM_ERR_UNSUPPORTED, "no plan for %d x %d x %d on %d SMs", T, N, K, sms);
     const int bn = how.bn, slots = sms * (bn <= 64 ? 2 : 1);
     const bool pair = how.pair;
     a.split = how.split;

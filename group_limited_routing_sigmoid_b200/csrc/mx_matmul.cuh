@@ -2,6 +2,7 @@
 // tile; mx_matmul_pair.cu: a CTA pair a tile).
 #pragma once
 
+#include "mx_plan.h"
 #include "ops_common.cuh"
 
 namespace beam {
@@ -9,11 +10,6 @@ namespace mx {
 
 using namespace ops;
 
-// Kinds of block-scaled MMA: NVFP4 (a scale per 16), MXFP4 (per 32) and
-// MXFP8 x MXFP8 / MXFP4 (per 32, 8-bit operands in shared memory).
-enum Kind { kNv = 0, kMx4 = 1, kMx8 = 2 };
-
-constexpr int kTileP = 128;               // rows of the A side per CTA
 constexpr int kRowBytes = 128;            // bytes of a row in a stage
 constexpr int kEpiWarps = 8;
 constexpr int kCopyWarp = 2 + kEpiWarps;

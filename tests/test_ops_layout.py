@@ -12,6 +12,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "group_limited_routing_sigmoid_b200", "csrc")
 
 HOST = r"""
+#include "mx_plan.h"
 #include "route_layout.h"
 #include <cstdint>
 #include <cstring>
@@ -39,6 +40,13 @@ extern "C" int walk(int E, int G, int keep, int *at)
     for (int e = 0; e < E; ++e)
         if (seen[e] != 1) return at[0] = e, at[1] = seen[e], 2;
     return 0;
+}
+
+// A plan's width, split and whether it is a pair's.
+extern "C" void make_plan(int kind, int P, int Q, int nst, int swap, int vec, int sms, int *out)
+{
+    const mx::Plan p = mx::plan(kind, P, Q, nst, swap != 0, vec != 0, sms);
+    out[0] = p.bn, out[1] = p.split, out[2] = p.pair;
 }
 """
 
@@ -80,3 +88,25 @@ def test_every_expert_has_one_lane_and_one_register(host):
                 count += 1
                 assert host.walk(E, G, keep, bad.ctypes.data_as(ctypes.c_void_p)) == 0, (E, G, keep, bad)
     assert count > 5000
+
+
+@pytest.mark.parametrize("sms", [1, 2, 7, 16, 74, 132, 148, 152, 160, 208])
+def test_every_product_has_a_plan(host, sms):
+    """Whatever the device's SM count: a width, a split of no more parts than K has stages, one B tile below 64 columns."""
+    out = np.zeros(3, np.int32)
+    at = out.ctypes.data_as(ctypes.c_void_p)
+    edges = {1, 2, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 1000, 4097, 37888, 37889, 38000, 38912, 38913, 100000, (1 << 27) - 1}
+    edges |= {128 * n + d for n in (sms, 2 * sms, 45, 93) for d in (-1, 0, 1)}
+    for T in (1, 5, 16, 17, 32, 33, 64, 65, 128, 129, 1021, 8192, 38000, 50000, (1 << 27) - 1):
+        for N in sorted(e for e in edges if e > 0):
+            swap = N >= T if T <= 128 or N <= 128 else False
+            P, Q = (N, T) if swap else (T, N)
+            for nst in (1, 2, 3, 7, 8, 80):
+                for kind in range(3):
+                    for vec in (0, 1):
+                        host.make_plan(kind, P, Q, nst, int(swap), vec, sms, at)
+                        bn, split, pair = out
+                        what = (kind, T, N, nst, vec, list(out))
+                        assert bn in ((256,) if pair else (16, 32, 64, 128)), what
+                        assert 1 <= split <= min(8, nst) and (bn >= 64 or bn >= Q), what
+                        assert not (pair and (swap or split > 1 or P <= 128 or Q <= 128)), what
