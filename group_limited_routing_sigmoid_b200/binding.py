@@ -38,7 +38,7 @@ SYMBOLS = (
     "beam_moe_profile_begin",
     "beam_moe_profile_end", "beam_moe_check_wait_timeout", "beam_moe_last_error",
     "beam_moe_create_error", "beam_moe_destroy",
-    "beam_mx_scale_bytes", "beam_mx_tensor_scale", "beam_mx_quantize", "beam_mx_dequantize",
+    "beam_mx_scale_bytes", "beam_mx_tensor_scale", "beam_mx_quantize", "beam_mx_quantize_nvfp4", "beam_mx_dequantize",
     "beam_mx_tile_scales", "beam_mx_matmul", "beam_rms_norm", "beam_route_scores",
     "beam_ops_status", "beam_ops_error",
 )
@@ -94,6 +94,7 @@ def library() -> ctypes.CDLL:
         lib.beam_mx_scale_bytes.argtypes = [I, L, I, I]
         lib.beam_mx_tensor_scale.argtypes = [P, P, I, L, I, L, P]
         lib.beam_mx_quantize.argtypes = [P, P, I, L, I, L, I, I, P, P, P]
+        lib.beam_mx_quantize_nvfp4.argtypes = [P, P, I, L, I, L, I, P, P, P]
         lib.beam_mx_dequantize.argtypes = [P, P, P, P, I, I, L, I, P, I, L]
         lib.beam_mx_tile_scales.argtypes = [P, I, P, L, I, P]
         lib.beam_mx_matmul.argtypes = [P, I, P, P, P, I, P, P, P, I, I, I, P, I, L]

@@ -325,9 +325,9 @@ __device__ __forceinline__ float tensor_scale_of(uint32_t amax_bits)
 }
 
 // ONE: the grid is one cluster, which joins its blocks' maxima itself; else out
-// holds zero beforehand and takes them by atomics.
+// holds zero beforehand and takes them by atomics.  The scale is `most` at most.
 template <typename T, bool ONE, int AL>
-__global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, float *out)
+__global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, float *out, const float most)
 {
     constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;
     // every block of the cluster has started before one writes into another's
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, f
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 1; i < kThreadsQ / 32; ++i) m = max(m, part[i]);
-        if constexpr (!ONE) atomicMax(reinterpret_cast<int *>(out), __float_as_int(tensor_scale_of(m)));
+        if constexpr (!ONE) atomicMax(reinterpret_cast<int *>(out), __float_as_int(fminf(tensor_scale_of(m), most)));
     }
     if constexpr (ONE) {
         __shared__ uint32_t all[kCluster];
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreadsQ) mx_amax_kernel(const QuantArgs p, f
         if (threadIdx.x == 0 && cluster_ctarank() == 0) {
 #pragma unroll
             for (int i = 0; i < kCluster; ++i) m = max(m, all[i]);
-            *out = tensor_scale_of(m);
+            *out = fminf(tensor_scale_of(m), most);
         }
     }
 }
@@ -547,10 +547,10 @@ cudaError_t launch_dequantize(const DequantArgs &a, int dtype, int al, cudaStrea
 #undef BEAM_ARGS
 }
 
-cudaError_t launch_amax(const QuantArgs &a, int dtype, int al, float *out, cudaStream_t s)
+cudaError_t launch_amax(const QuantArgs &a, int dtype, int al, float *out, float most, cudaStream_t s)
 {
     const dim3 grid(grid_for(a.chunks.total));
-#define BEAM_ARGS a, out
+#define BEAM_ARGS a, out, most
     return BEAM_TYPED(mx_amax_kernel, false);
 #undef BEAM_ARGS
 }
@@ -574,12 +574,12 @@ cudaError_t launch_cluster(void (*kernel)(K...), cudaStream_t s, Args... args)
 }
 
 template <typename T>
-cudaError_t launch_amax_one(const QuantArgs &a, int al, float *out, cudaStream_t s)
+cudaError_t launch_amax_one(const QuantArgs &a, int al, float *out, float most, cudaStream_t s)
 {
-    if (al == kFlat) return launch_cluster(mx_amax_kernel<T, true, kFlat>, s, a, out);
-    if (al == 32) return launch_cluster(mx_amax_kernel<T, true, 32>, s, a, out);
-    if (al == 16) return launch_cluster(mx_amax_kernel<T, true, 16>, s, a, out);
-    return launch_cluster(mx_amax_kernel<T, true, 0>, s, a, out);
+    if (al == kFlat) return launch_cluster(mx_amax_kernel<T, true, kFlat>, s, a, out, most);
+    if (al == 32) return launch_cluster(mx_amax_kernel<T, true, 32>, s, a, out, most);
+    if (al == 16) return launch_cluster(mx_amax_kernel<T, true, 16>, s, a, out, most);
+    return launch_cluster(mx_amax_kernel<T, true, 0>, s, a, out, most);
 }
 
 // launch(a) over slices of rows of `per` chunks each (rows == 1: over chunks;
@@ -615,6 +615,80 @@ int check_shape(int format, long long rows, int K, int layout)
     return BEAM_OK;
 }
 
+// What the arguments of a tensor scale have to hold.
+int check_scale(const void *x, int dtype, long long rows, int K, long long ldx, const float *tensor_scale)
+{
+    if (rows < 0 || rows > (1LL << 40) || K < 1) return fail(BEAM_ERR_INVALID_ARG, "rows must be >= 0 and K >= 1");
+    if (rows > kMostElements / K) return fail(BEAM_ERR_INVALID_ARG, "%lld x %d elements are too many", rows, K);
+    if (!dtype_ok(dtype)) return fail(BEAM_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (!tensor_scale || !aligned(tensor_scale, 4)) return fail(BEAM_ERR_INVALID_ARG, "tensor_scale is NULL or not aligned");
+    if (rows > 0 && (!x || !aligned(x, dtype_size(dtype)))) return fail(BEAM_ERR_INVALID_ARG, "x is NULL or not aligned");
+    if (rows > 0 && ldx < K) return fail(BEAM_ERR_INVALID_ARG, "ldx is below K");
+    return BEAM_OK;
+}
+
+int find_scale(cudaStream_t s, const void *x, int dtype, long long rows, int K, long long ldx, float *tensor_scale, float most)
+{
+    if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
+    const bool flat = rows == 1 || ldx == K;
+    QuantArgs a{x, nullptr, nullptr, nullptr, rows, ldx, K, 0, Chunks(0, 1), ScaleMap(0, 1)};
+    const int al = chunk_alignment(x, flat, ldx, dtype);
+    if (flat) a.rows = 1, a.K = rows * (long long)K;
+    const long long per = (a.K + kChunk - 1) / kChunk;
+    if (a.rows * per <= kOneCluster) {
+        if (a.rows > 0) a.chunks = Chunks((int)a.rows, (int)per);
+        const cudaError_t one = dtype == BEAM_BF16  ? launch_amax_one<__nv_bfloat16>(a, al, tensor_scale, most, s)
+                                : dtype == BEAM_F16 ? launch_amax_one<__half>(a, al, tensor_scale, most, s)
+                                                    : launch_amax_one<float>(a, al, tensor_scale, most, s);
+        return check_cuda(one, "beam_mx_tensor_scale");
+    }
+    if (int rc = check_cuda(cudaMemsetAsync(tensor_scale, 0, sizeof(float), s), "cudaMemsetAsync")) return rc;
+    const auto launch = [&](const QuantArgs &part) { return launch_amax(part, dtype, al, tensor_scale, most, s); };
+    const cudaError_t e = in_slices(a, a.rows, per, [&](QuantArgs &part, long long c) {
+        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
+        part.K -= c * kChunk;
+    }, launch);
+    return check_cuda(e, "beam_mx_tensor_scale");
+}
+
+// What the arguments of a quantisation of one row and more have to hold.
+int check_quantize(const void *x, int dtype, int K, long long ldx, int format, const float *tensor_scale, const uint8_t *codes,
+                   const uint8_t *scales)
+{
+    if (!x || !codes || !scales) return fail(BEAM_ERR_INVALID_ARG, "x, codes and scales are required");
+    if ((format == BEAM_NVFP4) != (tensor_scale != nullptr))
+        return fail(BEAM_ERR_INVALID_ARG, "tensor_scale is required for NVFP4 and must be NULL for the others");
+    if (ldx < K) return fail(BEAM_ERR_INVALID_ARG, "ldx is below K");
+    if (!aligned(x, dtype_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(tensor_scale, 4))
+        return fail(BEAM_ERR_INVALID_ARG, "a pointer is not aligned");
+    return BEAM_OK;
+}
+
+cudaError_t quantize(cudaStream_t s, const void *x, int dtype, long long rows, int K, long long ldx, int format, int layout,
+                     const float *tensor_scale, uint8_t *codes, uint8_t *scales)
+{
+    const int n = K / block_of(format);
+    const bool flat = layout == BEAM_SCALES_ROWS && (rows == 1 || ldx == K);
+    QuantArgs a{x, tensor_scale, codes, scales, rows, ldx, K, 0, Chunks(), ScaleMap(layout, n)};
+    const int al = chunk_alignment(x, flat, ldx, dtype);
+    const auto launch = [&](const QuantArgs &part) {
+        return format == BEAM_NVFP4   ? launch_quantize<BEAM_NVFP4>(part, dtype, al, s)
+               : format == BEAM_MXFP4 ? launch_quantize<BEAM_MXFP4>(part, dtype, al, s)
+                                      : launch_quantize<BEAM_MXFP8>(part, dtype, al, s);
+    };
+    // tiled: the chunks cover the tiles' padding rows and scales too
+    const bool tiled = layout == BEAM_SCALES_TILED;
+    if (flat) a.rows = 1, a.K = rows * (long long)K;
+    const long long all = flat ? 1 : tiled ? (rows + 127) / 128 * 128 : rows;
+    const long long per = tiled ? (long long)a.map.n4 * 4 * block_of(format) / kChunk : a.K / kChunk;
+    return in_slices(a, all, per, [&](QuantArgs &part, long long c) {
+        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
+        part.codes = codes + (format == BEAM_MXFP8 ? c * kChunk : c * kChunk / 2);
+        part.scales = scales + c * kChunk / block_of(format);
+        part.K -= c * kChunk;
+    }, launch);
+}
+
 }  // namespace
 }  // namespace beam
 
@@ -634,33 +708,8 @@ int beam_mx_tensor_scale(void *stream, const void *x, int dtype, long long rows,
 {
     using namespace beam;
     using namespace beam::ops;
-    if (rows < 0 || rows > (1LL << 40) || K < 1) return fail(BEAM_ERR_INVALID_ARG, "rows must be >= 0 and K >= 1");
-    if (rows > kMostElements / K) return fail(BEAM_ERR_INVALID_ARG, "%lld x %d elements are too many", rows, K);
-    if (!dtype_ok(dtype)) return fail(BEAM_ERR_INVALID_ARG, "dtype %d", dtype);
-    if (!tensor_scale || !aligned(tensor_scale, 4)) return fail(BEAM_ERR_INVALID_ARG, "tensor_scale is NULL or not aligned");
-    if (rows > 0 && (!x || !aligned(x, dtype_size(dtype)))) return fail(BEAM_ERR_INVALID_ARG, "x is NULL or not aligned");
-    if (rows > 0 && ldx < K) return fail(BEAM_ERR_INVALID_ARG, "ldx is below K");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
-    const bool flat = rows == 1 || ldx == K;
-    QuantArgs a{x, nullptr, nullptr, nullptr, rows, ldx, K, 0, Chunks(0, 1), ScaleMap(0, 1)};
-    const int al = chunk_alignment(x, flat, ldx, dtype);
-    if (flat) a.rows = 1, a.K = rows * (long long)K;
-    const long long per = (a.K + kChunk - 1) / kChunk;
-    if (a.rows * per <= kOneCluster) {
-        if (a.rows > 0) a.chunks = Chunks((int)a.rows, (int)per);
-        const cudaError_t one = dtype == BEAM_BF16  ? launch_amax_one<__nv_bfloat16>(a, al, tensor_scale, s)
-                                : dtype == BEAM_F16 ? launch_amax_one<__half>(a, al, tensor_scale, s)
-                                                    : launch_amax_one<float>(a, al, tensor_scale, s);
-        return check_cuda(one, "beam_mx_tensor_scale");
-    }
-    if (int rc = check_cuda(cudaMemsetAsync(tensor_scale, 0, sizeof(float), s), "cudaMemsetAsync")) return rc;
-    const auto launch = [&](const QuantArgs &part) { return launch_amax(part, dtype, al, tensor_scale, s); };
-    const cudaError_t e = in_slices(a, a.rows, per, [&](QuantArgs &part, long long c) {
-        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
-        part.K -= c * kChunk;
-    }, launch);
-    return check_cuda(e, "beam_mx_tensor_scale");
+    if (int rc = check_scale(x, dtype, rows, K, ldx, tensor_scale)) return rc;
+    return find_scale(static_cast<cudaStream_t>(stream), x, dtype, rows, K, ldx, tensor_scale, INFINITY);
 }
 
 int beam_mx_quantize(void *stream, const void *x, int dtype, long long rows, int K, long long ldx,
@@ -671,35 +720,26 @@ int beam_mx_quantize(void *stream, const void *x, int dtype, long long rows, int
     if (int rc = check_shape(format, rows, K, layout)) return rc;
     if (!dtype_ok(dtype)) return fail(BEAM_ERR_INVALID_ARG, "dtype %d", dtype);
     if (rows == 0) return BEAM_OK;
-    if (!x || !codes || !scales) return fail(BEAM_ERR_INVALID_ARG, "x, codes and scales are required");
-    if ((format == BEAM_NVFP4) != (tensor_scale != nullptr))
-        return fail(BEAM_ERR_INVALID_ARG, "tensor_scale is required for NVFP4 and must be NULL for the others");
-    if (ldx < K) return fail(BEAM_ERR_INVALID_ARG, "ldx is below K");
-    if (!aligned(x, dtype_size(dtype)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(tensor_scale, 4))
-        return fail(BEAM_ERR_INVALID_ARG, "a pointer is not aligned");
+    if (int rc = check_quantize(x, dtype, K, ldx, format, tensor_scale, codes, scales)) return rc;
     if (!sm_count()) return fail(BEAM_ERR_CUDA, "no CUDA device");
-    const int n = K / block_of(format);
-    const bool flat = layout == BEAM_SCALES_ROWS && (rows == 1 || ldx == K);
-    QuantArgs a{x, tensor_scale, codes, scales, rows, ldx, K, 0, Chunks(), ScaleMap(layout, n)};
-    const int al = chunk_alignment(x, flat, ldx, dtype);
+    return check_cuda(quantize(static_cast<cudaStream_t>(stream), x, dtype, rows, K, ldx, format, layout, tensor_scale, codes, scales),
+                      "beam_mx_quantize");
+}
+
+int beam_mx_quantize_nvfp4(void *stream, const void *x, int dtype, long long rows, int K, long long ldx, int layout,
+                           float *tensor_scale, uint8_t *codes, uint8_t *scales)
+{
+    using namespace beam;
+    using namespace beam::ops;
+    if (int rc = check_shape(BEAM_NVFP4, rows, K, layout)) return rc;
+    if (int rc = check_scale(x, dtype, rows, K, ldx, tensor_scale)) return rc;
+    if (rows > 0)
+        if (int rc = check_quantize(x, dtype, K, ldx, BEAM_NVFP4, tensor_scale, codes, scales)) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto launch = [&](const QuantArgs &part) {
-        return format == BEAM_NVFP4   ? launch_quantize<BEAM_NVFP4>(part, dtype, al, s)
-               : format == BEAM_MXFP4 ? launch_quantize<BEAM_MXFP4>(part, dtype, al, s)
-                                      : launch_quantize<BEAM_MXFP8>(part, dtype, al, s);
-    };
-    // tiled: the chunks cover the tiles' padding rows and scales too
-    const bool tiled = layout == BEAM_SCALES_TILED;
-    if (flat) a.rows = 1, a.K = rows * (long long)K;
-    const long long all = flat ? 1 : tiled ? (rows + 127) / 128 * 128 : rows;
-    const long long per = tiled ? (long long)a.map.n4 * 4 * block_of(format) / kChunk : a.K / kChunk;
-    const cudaError_t e = in_slices(a, all, per, [&](QuantArgs &part, long long c) {
-        part.x = static_cast<const uint8_t *>(x) + c * kChunk * dtype_size(dtype);
-        part.codes = codes + (format == BEAM_MXFP8 ? c * kChunk : c * kChunk / 2);
-        part.scales = scales + c * kChunk / block_of(format);
-        part.K -= c * kChunk;
-    }, launch);
-    return check_cuda(e, "beam_mx_quantize");
+    // at most what quantize_chunk's arithmetic takes: larger values saturate
+    if (int rc = find_scale(s, x, dtype, rows, K, ldx, tensor_scale, kMaxTensorScale)) return rc;
+    if (rows == 0) return BEAM_OK;
+    return check_cuda(quantize(s, x, dtype, rows, K, ldx, BEAM_NVFP4, layout, tensor_scale, codes, scales), "beam_mx_quantize_nvfp4");
 }
 
 int beam_mx_dequantize(void *stream, const uint8_t *codes, const uint8_t *scales,

@@ -24,6 +24,7 @@ struct Library {
     decltype(&beam_rms_norm) rms_norm;
     decltype(&beam_mx_tensor_scale) tensor_scale;
     decltype(&beam_mx_quantize) quantize;
+    decltype(&beam_mx_quantize_nvfp4) quantize_nvfp4;
     decltype(&beam_mx_dequantize) dequantize;
     decltype(&beam_mx_tile_scales) tile_scales;
     decltype(&beam_mx_matmul) matmul;
@@ -368,26 +369,21 @@ PyObject *rms_norm(PyObject *const *a, Py_ssize_t n)
 }
 
 // x, out -> out
-at::Tensor find_scale(const at::Tensor &x, const Rows &r, PyObject *given, const On &on)
-{
-    at::Tensor out;
-    if (given == Py_None) {
-        out = fresh({1}, at::kFloat, x);
-    } else {
-        flat<float>(given, "out", at::kFloat, 1, &x);
-        out = THPVariable_Unpack(given);
-    }
-    check(lib.tensor_scale(on.stream, r.p, r.code, r.rows, r.columns("x"), r.ld, static_cast<float *>(out.data_ptr())));
-    return out;
-}
-
 PyObject *tensor_scale(PyObject *const *a, Py_ssize_t n)
 {
     need(n, 2);
     const at::Tensor &x = tensor(a[0], "x", nullptr);
     const Rows r(x, "x");
     const On on(x);
-    return THPVariable_Wrap(find_scale(x, r, a[1], on));
+    at::Tensor out;
+    if (a[1] == Py_None) {
+        out = fresh({1}, at::kFloat, x);
+    } else {
+        flat<float>(a[1], "out", at::kFloat, 1, &x);
+        out = THPVariable_Unpack(a[1]);
+    }
+    check(lib.tensor_scale(on.stream, r.p, r.code, r.rows, r.columns("x"), r.ld, static_cast<float *>(out.data_ptr())));
+    return THPVariable_Wrap(out);
 }
 
 // x, format, layout, tensor_scale, codes, scales, the format's and the layout's names -> MxTensor
@@ -399,18 +395,16 @@ PyObject *quantize(PyObject *const *a, Py_ssize_t n)
     const int format = small_integer(a[1]), layout = small_integer(a[2]);
     const On on(x);
     Operand q = new_operand(a[4], a[5], format, layout, r.rows, r.cols, x);
+    const int K = r.columns("x");
     at::Tensor scale;
-    const float *g = nullptr;
-    if (format == BEAM_NVFP4) {
-        if (a[3] == Py_None) {
-            scale = find_scale(x, r, Py_None, on);
-        } else {
-            flat<float>(a[3], "tensor_scale", at::kFloat, 1, &x);
-            scale = THPVariable_Unpack(a[3]);
-        }
-        g = static_cast<const float *>(scale.data_ptr());
+    if (format == BEAM_NVFP4 && a[3] == Py_None) {
+        scale = fresh({1}, at::kFloat, x);
+        check(lib.quantize_nvfp4(on.stream, r.p, r.code, r.rows, K, r.ld, layout, static_cast<float *>(scale.data_ptr()), q.c, q.s));
+    } else {
+        const float *g = format == BEAM_NVFP4 ? flat<float>(a[3], "tensor_scale", at::kFloat, 1, &x) : nullptr;
+        if (g) scale = THPVariable_Unpack(a[3]);
+        check(lib.quantize(on.stream, r.p, r.code, r.rows, K, r.ld, format, layout, g, q.c, q.s));
     }
-    check(lib.quantize(on.stream, r.p, r.code, r.rows, r.columns("x"), r.ld, format, layout, g, q.c, q.s));
     return pack_operand(q, a[6], a[7], r.rows, r.cols, scale);
 }
 

@@ -78,7 +78,7 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(BeamMoEError, NormResult, MxTensor, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.beam_rms_norm, lib.beam_mx_tensor_scale, lib.beam_mx_quantize, lib.beam_mx_dequantize,
+            lib.beam_rms_norm, lib.beam_mx_tensor_scale, lib.beam_mx_quantize, lib.beam_mx_quantize_nvfp4, lib.beam_mx_dequantize,
             lib.beam_mx_tile_scales, lib.beam_mx_matmul, lib.beam_route_scores, lib.beam_ops_error)))
         _binding = module
     return _binding
@@ -152,7 +152,10 @@ def _given(q, name: str, format: str, layout: str, x):
 
 
 def mx_tensor_scale(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The NVFP4 scale of x [rows, K]: the least power of two g with amax <= 6 * 448 * g (fp32 [1])."""
+    """The NVFP4 scale of x [rows, K]: the least power of two g with amax <= 6 * 448 * g (fp32 [1]).
+
+    With elements above 1.4e37 it is above 2^112, under which mx_quantize gives
+    NaN; mx_quantize finding the scale itself stops at 2^112."""
     f = (_binding or _native()).tensor_scale
     return f(x, out) if stream is None else _elsewhere(stream, f, x, out)
 
@@ -161,8 +164,8 @@ def mx_quantize(x: torch.Tensor, format: str, layout: str = "rows", tensor_scale
                 out: Optional[MxTensor] = None, stream=None) -> MxTensor:
     """x [rows, K] (bf16, fp16 or fp32, rows may be strided) to a microscaled operand.
 
-    NVFP4 without a `tensor_scale` (fp32 [1]) finds one first (mx_tensor_scale:
-    one more pass over x).  layout "rows" is what BeamMoE.nvfp4 and checkpoints
+    NVFP4 without a `tensor_scale` (fp32 [1]) finds one first (mx_tensor_scale,
+    2^112 at most: one more pass over x).  layout "rows" is what BeamMoE.nvfp4 and checkpoints
     take, "tiled" what mx_matmul takes.  `out`: an operand of the same shape to
     write into (its tensor_scale is not)."""
     f, lay = _key(FORMATS, format, "format"), _key(LAYOUTS, layout, "layout")

@@ -60,6 +60,8 @@ long long beam_mx_scale_bytes(int format, long long rows, int K, int layout);
  * magnitude, taken as 2^-100 at least.  A power of two costs at most one of
  * the E4M3 scale's 17 binades and keeps every decision of beam_mx_quantize
  * and every product element * scale * g exact.
+ * Elements above 6 * 448 * 2^112 (1.4e37) give a g above 2^112, which
+ * beam_mx_quantize does not take; beam_mx_quantize_nvfp4 stops there.
  * tensor_scale  fp32 [1] (out).  rows >= 0, K >= 1; an empty tensor gives the
  *               scale of amax = 2^-100.
  */
@@ -86,6 +88,16 @@ int beam_mx_tensor_scale(void *stream, const void *x, int dtype, long long rows,
 int beam_mx_quantize(void *stream, const void *x, int dtype, long long rows, int K, long long ldx,
                      int format, int layout, const float *tensor_scale, uint8_t *codes,
                      uint8_t *scales);
+
+/*
+ * x to NVFP4 under the scale that beam_mx_tensor_scale finds, 2^112 at most:
+ * finite elements beyond 6 * 448 * 2^112 saturate there.  One more pass over x.
+ * tensor_scale  fp32 [1], device (out).  The rest as in beam_mx_quantize; with
+ *               rows = 0 only tensor_scale is written.
+ */
+int beam_mx_quantize_nvfp4(void *stream, const void *x, int dtype, long long rows, int K,
+                           long long ldx, int layout, float *tensor_scale, uint8_t *codes,
+                           uint8_t *scales);
 
 /*
  * The values that codes and scales stand for, out [rows, K] (dtype, rows ldo

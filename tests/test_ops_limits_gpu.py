@@ -82,3 +82,42 @@ def test_route_sums_that_lose_their_small_terms():
     bias = torch.zeros(E)
     bias[200], bias[300] = 1 - 47 * 2.0 ** -24, 0.5    # the second: what is not chosen lies far below
     check_route(l.cuda(), 2, "softmax", bias.cuda(), G, 16, 2, False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.float16])
+@pytest.mark.parametrize("layout", ["rows", "tiled"])
+@pytest.mark.parametrize("rows", [3, 700])
+def test_found_scales_stay_in_the_quantisers_range(dtype, layout, rows):
+    """NVFP4 of tensors that hold their type's largest or lowest value (a mask's, say), the scale found: no finite element
+    reads back as NaN or infinity, and the blocks without it are quantised under the scale that is returned."""
+    K = 1024                                           # 700 rows: more than one cluster finds the scale of
+    for big in (torch.finfo(dtype).max, torch.finfo(dtype).min, 1.5e37, 1.0):
+        x = torch.randn(rows, K, generator=torch.Generator().manual_seed(rows)) * 3
+        x[rows // 2, K - 1] = big
+        x = x.clamp(torch.finfo(dtype).min, torch.finfo(dtype).max).to(dtype).cuda()
+        q = ops.mx_quantize(x, "nvfp4", layout)
+        g = min(R.tensor_scale(f64(x)), 2.0 ** 112)
+        assert float(q.tensor_scale) == g
+        e, sb = R.quantize(f64(x), "nvfp4", g)
+        np.testing.assert_array_equal(q.scales.cpu().numpy(), sb.astype(np.uint8) if layout == "rows" else R.tile(sb))
+        np.testing.assert_array_equal(R.elements(q.codes.cpu().numpy(), "nvfp4"), e)
+        v = ops.mx_dequantize(q, torch.float32)
+        assert v.isfinite().all() and (v[rows // 2, K - 1] > 0) == (big > 0)
+        given = ops.mx_quantize(x, "nvfp4", layout, tensor_scale=q.tensor_scale)
+        assert torch.equal(given.codes, q.codes) and torch.equal(given.scales, q.scales)
+
+
+def test_found_scales_captured():
+    """The scale of a tensor above one cluster's size is a memset and a kernel; both and the quantiser replay on new values."""
+    x = torch.randn(300, 4096, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q = ops.mx_quantize(x, "nvfp4", "tiled")
+        v = ops.mx_dequantize(q)
+    for scale in (1.0, 30.0, 0.01):
+        x.mul_(scale)
+        g.replay()
+        torch.cuda.synchronize()
+        want = ops.mx_quantize(x, "nvfp4", "tiled")
+        assert torch.equal(q.tensor_scale, want.tensor_scale) and torch.equal(q.codes, want.codes)
+        assert torch.equal(q.scales, want.scales) and torch.equal(v, ops.mx_dequantize(want))

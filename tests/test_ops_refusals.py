@@ -1,0 +1,28 @@
+"""Refusals of the handle-free operators' entry points: host checks run before any CUDA call, so none of this needs a GPU."""
+import ctypes
+
+import pytest
+
+from group_limited_routing_sigmoid_b200 import binding
+from group_limited_routing_sigmoid_b200.build import build
+
+INVALID = binding.BEAM_ERR_INVALID_ARG
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build(quiet=True)
+    return binding.library()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=None), dict(codes=None), dict(scales=None), dict(g=None), dict(dtype=3), dict(rows=-1), dict(K=24), dict(K=0),
+    dict(ldx=32), dict(layout=2), dict(x=17), dict(codes=24), dict(scales=18), dict(g=18), dict(rows=1 << 40, K=1 << 30, ldx=1 << 30),
+])
+def test_quantize_nvfp4_refuses(lib, kw):
+    a = dict(x=16, dtype=0, rows=4, K=64, ldx=64, layout=0, g=16, codes=16, scales=16)
+    a.update(kw)
+    x, g, codes, scales = (a[n] and P(a[n]) for n in ("x", "g", "codes", "scales"))
+    assert lib.beam_mx_quantize_nvfp4(None, x, a["dtype"], a["rows"], a["K"], a["ldx"], a["layout"], g, codes, scales) == INVALID
+    assert lib.beam_ops_error()
