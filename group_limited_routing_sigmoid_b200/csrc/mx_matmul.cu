@@ -41,8 +41,14 @@ namespace {
 
 using namespace mx;
 
-// Sticky status word of the device (beam_ops_status).
+// Sticky status word of the device (beam_ops_status), and where callers that
+// take it, each with a slot of its own, find what it held.
+constexpr int kTakers = 1024;
 __device__ int g_ops_status;
+__device__ int g_ops_taken[kTakers];
+
+// Read and cleared in one step: of several callers one gets an event.
+__global__ void take_status_kernel(int slot) { g_ops_taken[slot] = atomicExch(&g_ops_status, 0); }
 
 template <int KIND, int BN>
 struct Cfg {
@@ -580,16 +586,17 @@ extern "C" int beam_ops_status(void *stream)
 {
     using namespace beam;
     using namespace beam::ops;
+    static std::atomic<unsigned> ticket{0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    if (int rc = check_cuda(cudaStreamIsCapturing(s, &capturing), "beam_ops_status")) return rc;
+    if (capturing != cudaStreamCaptureStatusNone) return fail(BEAM_ERR_INVALID_ARG, "beam_ops_status: the stream is being captured");
+    const int slot = (int)(ticket.fetch_add(1, std::memory_order_relaxed) % kTakers);
     int host = 0;
-    const int zero = 0;
-    if (int rc = check_cuda(cudaMemcpyFromSymbolAsync(&host, g_ops_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s),
+    take_status_kernel<<<1, 1, 0, s>>>(slot);
+    if (int rc = check_cuda(cudaGetLastError(), "beam_ops_status")) return rc;
+    if (int rc = check_cuda(cudaMemcpyFromSymbolAsync(&host, g_ops_taken, sizeof(int), slot * sizeof(int), cudaMemcpyDeviceToHost, s),
                             "beam_ops_status")) return rc;
     if (int rc = check_cuda(cudaStreamSynchronize(s), "beam_ops_status")) return rc;
-    if (host != 0) {
-        if (int rc = check_cuda(cudaMemcpyToSymbolAsync(g_ops_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s),
-                                "beam_ops_status")) return rc;
-        if (int rc = check_cuda(cudaStreamSynchronize(s), "beam_ops_status")) return rc;
-    }
     return host;
 }

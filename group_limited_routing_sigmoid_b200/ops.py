@@ -113,7 +113,13 @@ def _used(stream, *values):
 
 
 def ops_status(device=None, stream=None) -> int:
-    """Wait for `stream`, then read and clear the device's status word."""
+    """Wait for `stream`, then read and clear the device's status word.
+
+    0, or BEAM_ERR_TIMEOUT when a bounded wait inside mx_matmul ran out since
+    the last call.  mx_matmul does not look at the word itself (that would wait
+    for the GPU): the result of that product, and of every later one on the
+    device until this call, is not valid and raises nothing, so a program looks
+    here where it synchronises anyway, before it uses what it computed."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(device):
         if stream is None:
@@ -197,7 +203,9 @@ def mx_tile_scales(q: MxTensor, stream=None) -> MxTensor:
 
 def mx_matmul(a: MxTensor, w: MxTensor, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
-    """a [T, K] . w [N, K]^T -> [T, N]: NVFP4 x NVFP4, MXFP4 x MXFP4, MXFP8 x MXFP4 or MXFP8 x MXFP8, scales tiled."""
+    """a [T, K] . w [N, K]^T -> [T, N]: NVFP4 x NVFP4, MXFP4 x MXFP4, MXFP8 x MXFP4 or MXFP8 x MXFP8, scales tiled.
+
+    Its waits on the GPU are bounded; whether one ran out, ops_status tells."""
     d = _key(DTYPES, dtype, "dtype")
     f = (_binding or _native()).matmul
     return f(a, w, d, out) if stream is None else _elsewhere(stream, f, a, w, d, out)

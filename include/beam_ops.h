@@ -187,7 +187,10 @@ int beam_route_scores(void *stream, const float *logits, int T, int E, long long
  * Synchronise `stream`, then return and clear the current device's status
  * word of these operators: BEAM_OK, or BEAM_ERR_TIMEOUT when a bounded wait
  * inside beam_mx_matmul ran out since the last call.  The result of that
- * product, and of those that ran after it before this call, is not valid.
+ * product, and of those that ran after it before this call, is not valid.  The
+ * word is read and cleared in one step: one of several callers gets an event.
+ * A stream that is being captured is refused (BEAM_ERR_INVALID_ARG) and its
+ * capture goes on.
  */
 int beam_ops_status(void *stream);
 

@@ -6,6 +6,7 @@ import torch
 
 import ops_ref as R
 from group_limited_routing_sigmoid_b200 import ops
+from group_limited_routing_sigmoid_b200.binding import BEAM_ERR_INVALID_ARG
 from group_limited_routing_sigmoid_b200.build import build
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +122,16 @@ def test_found_scales_captured():
         want = ops.mx_quantize(x, "nvfp4", "tiled")
         assert torch.equal(q.tensor_scale, want.tensor_scale) and torch.equal(q.codes, want.codes)
         assert torch.equal(q.scales, want.scales) and torch.equal(v, ops.mx_dequantize(want))
+
+
+def test_status_is_refused_in_a_capture_that_goes_on():
+    x = torch.randn(64, 512, generator=torch.Generator().manual_seed(1)).cuda()
+    want = ops.mx_quantize(x, "mxfp8")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        assert ops.ops_status() == BEAM_ERR_INVALID_ARG
+        q = ops.mx_quantize(x, "mxfp8")
+    g.replay()
+    assert ops.ops_status() == 0
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
