@@ -40,7 +40,7 @@ SYMBOLS = (
     "beam_moe_create_error", "beam_moe_destroy",
     "beam_mx_scale_bytes", "beam_mx_tensor_scale", "beam_mx_quantize", "beam_mx_quantize_nvfp4", "beam_mx_dequantize",
     "beam_mx_tile_scales", "beam_mx_matmul", "beam_rms_norm", "beam_route_scores",
-    "beam_ops_status", "beam_ops_error",
+    "beam_ops_status", "beam_ops_debug_withhold", "beam_ops_error",
 )
 
 _lib = None
@@ -101,6 +101,7 @@ def library() -> ctypes.CDLL:
         lib.beam_rms_norm.argtypes = [P, P, I, L, P, I, L, P, L, F, F, P, F, I, I, P, I, L, P, P, I]
         lib.beam_route_scores.argtypes = [P, P, I, I, L, I, P, I, I, I, I, I, F, P, P]
         lib.beam_ops_status.argtypes = [P]
+        lib.beam_ops_debug_withhold.argtypes = [I, I]
         lib.beam_ops_error.argtypes = []
         for name in SYMBOLS:
             getattr(lib, name).restype = I

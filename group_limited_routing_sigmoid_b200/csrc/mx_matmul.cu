@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
     uint64_t *scaled = drain + 2;   // a stage's scales are in tensor memory (and its codes in shared)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scaled + C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const WaitCtl ctl{p.status, kWaitLimitNs};
+    const WaitCtl ctl{p.status, p.limit_ns};
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
 
     if (warp == 0 && lane == 0) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     }
                     const uint32_t sp = base + stage * C::STAGE, sq = sp + C::P_BYTES, sf = sq + C::Q_BYTES;
                     const uint32_t fb = smem_u32(&full[stage]);
-                    mbar_arrive_expect_tx(fb, p.tx);
+                    mbar_arrive_expect_tx(fb, ks == p.withheld ? p.tx + kWithheldBytes : p.tx);
                     // x: bytes for the byte maps, elements for the 4-bit map (both 128 a stage)
                     tma_load_2d(sp, &maps.p, ks * kRowBytes, pt * kTileP, fb, pol_p);
                     tma_load_2d(sq, &maps.q, ks * kRowBytes, qt * BN, fb, pol_q);
@@ -239,14 +239,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<KIND, BN>::CTAS_PER_SM))
                     if (++stage == C::STAGES) stage = 0, phase ^= 1u;
                 }
             }
-            if (!ok) {
-                // copies in flight land before the CTA leaves
-                long long n = issued < C::STAGES ? issued : C::STAGES;
-                for (; n > 0; --n) {
-                    if (stage == 0) stage = C::STAGES - 1, phase ^= 1u;
-                    else --stage;
-                    mbar_wait_drain(smem_u32(&full[stage]), phase, ctl.limit_ns);
-                }
+            // copies in flight land before the CTA leaves, also those whose
+            // readers gave up after this thread had issued its last
+            for (long long n = issued < C::STAGES ? issued : C::STAGES; n > 0; --n) {
+                if (stage == 0) stage = C::STAGES - 1, phase ^= 1u;
+                else --stage;
+                mbar_wait_drain(smem_u32(&full[stage]), phase, ctl.limit_ns);
             }
         }
     } else if (warp == 1) {
@@ -483,6 +481,9 @@ cudaError_t launch_bn(int bn, const Maps &m, const MatmulArgs &a, int ctas, cuda
     }
 }
 
+// beam_ops_debug_withhold's, for the thread's next product.
+thread_local int t_withheld = -1, t_limit_ms = 0;
+
 // Device address of the status word, looked up once per device.
 std::atomic<int *> g_status_ptr[64];
 
@@ -564,6 +565,9 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
     // a spread copy counts the bytes of its packed codes
     a.tx = (uint32_t)(kTileP * (p_spread ? kRowBytes / 2 : kRowBytes) + q_box * (q_spread ? kRowBytes / 2 : kRowBytes) +
                       cps * 512 * (1 + q_blocks));
+    a.withheld = t_withheld;
+    a.limit_ns = t_withheld < 0 ? kWaitLimitNs : t_limit_ms * 1000000ll;
+    t_withheld = -1;
     Maps m;
     if (!code_map(&m.p, swap ? w_codes : a_codes, swap ? w_format : a_format, p_spread, a.P, K, kTileP) ||
         !code_map(&m.q, swap ? a_codes : w_codes, swap ? a_format : w_format, q_spread, a.Q, K, q_box) ||
@@ -580,6 +584,16 @@ extern "C" int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes
     else if (kind == kMx4) e = launch_bn<kMx4>(bn, m, a, ctas, s);
     else e = launch_bn<kMx8>(bn, m, a, ctas, s);
     return check_cuda(e, "beam_mx_matmul");
+}
+
+extern "C" int beam_ops_debug_withhold(int stage, int limit_ms)
+{
+    using namespace beam;
+    using namespace beam::ops;
+    if (stage < -1 || limit_ms < 1 || limit_ms > 2000)
+        return fail(BEAM_ERR_INVALID_ARG, "stage must be >= -1 and limit_ms in 1 .. 2000, got %d, %d", stage, limit_ms);
+    t_withheld = stage, t_limit_ms = limit_ms;
+    return BEAM_OK;
 }
 
 extern "C" int beam_ops_status(void *stream)

@@ -15,6 +15,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kCopyWarp = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr long long kWaitLimitNs = 2000000000ll;
+constexpr uint32_t kWithheldBytes = 16;
 
 // 512-byte scale tiles (128 rows x 4 scales) per stage and 128 rows.
 constexpr int tiles_per_stage(int kind) { return kind == kNv ? 4 : kind == kMx4 ? 2 : 1; }
@@ -43,6 +44,8 @@ struct MatmulArgs {
     int vec;               // 1: rows of out start on 16-byte boundaries
     uint32_t idesc;
     uint32_t tx;           // bytes one CTA's copies of a stage complete
+    int withheld;          // the stage of K that waits for more than that (beam_ops_debug_withhold), or -1
+    long long limit_ns;    // of a wait
 };
 
 cudaError_t launch_pair(int kind, const Maps &m, const MatmulArgs &a, int sms, cudaStream_t s);

@@ -49,10 +49,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *drain = tempty + 1;
     uint64_t *scaled = drain + 2;   // a stage's scales are in both CTAs' tensor memory
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(scaled + C::STAGES);
+    volatile uint32_t *gave_up = tmem_slot + 1;   // a wait of this CTA ran out
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();   // 0 issues the MMAs
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const WaitCtl ctl{p.status, kWaitLimitNs};
+    const WaitCtl ctl{p.status, p.limit_ns};
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -63,6 +64,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(tfull), 1);
         mbar_init(smem_u32(tempty), 2 * 32 * kEpiWarps);
         for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&drain[a]), 1);
+        *gave_up = 0;
         fence_barrier_init();
         tma_prefetch_desc(&maps.p);
         tma_prefetch_desc(&maps.q);
@@ -102,7 +104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t sp = base + stage * C::STAGE, sq = sp + C::HALF, sf = sq + C::HALF;
                     const uint32_t fl = smem_u32(&full[stage]), f = mapa_shared(fl, 0);   // CTA 0's barrier
-                    if (rank == 0) mbar_arrive_expect_tx(fl, 2u * p.tx);
+                    if (rank == 0) mbar_arrive_expect_tx(fl, 2u * p.tx + (ks == p.withheld ? kWithheldBytes : 0u));
                     tma_load_2d_pair(sp, &maps.p, ks * kRowBytes, prow, f, pol);
                     tma_load_2d_pair(sq, &maps.q, ks * kRowBytes, qrow, f, pol);
                     tma_load_3d_pair(sf, &maps.sp, ks * CPS, prow >> 7, f);
@@ -112,14 +114,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (++stage == C::STAGES) stage = 0, phase ^= 1u;
                 }
             }
-            if (!ok && rank == 0) {
-                // copies in flight (CTA 0's barriers count both CTAs') land before the pair leaves
-                long long n = issued < C::STAGES ? issued : C::STAGES;
-                for (; n > 0; --n) {
-                    if (stage == 0) stage = C::STAGES - 1, phase ^= 1u;
-                    else --stage;
-                    mbar_wait_drain(smem_u32(&full[stage]), phase, ctl.limit_ns);
-                }
+            if (!ok) *gave_up = 1;
+            // copies in flight (CTA 0's barriers count both CTAs') land before the pair leaves, also
+            // those whose readers gave up after this thread had issued its last
+            for (long long n = rank != 0 ? 0 : issued < C::STAGES ? issued : C::STAGES; n > 0; --n) {
+                if (stage == 0) stage = C::STAGES - 1, phase ^= 1u;
+                else --stage;
+                mbar_wait_drain(smem_u32(&full[stage]), phase, ctl.limit_ns);
             }
         }
     } else if (warp == 1) {
@@ -177,7 +178,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t iter = 0;
         for (int item = pair; item < total; item += npairs, ++iter) {
             const bool ok = mbar_wait(smem_u32(tfull), iter & 1u, ctl);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!__all_sync(0xffffffffu, ok)) {
+                *gave_up = 1;
+                break;
+            }
             tc_fence_after();
             const int pt = item % p.p_tiles, qt = item / p.p_tiles;
             const int prow0 = pt * 256 + (int)rank * 128 + quad * 32;
@@ -211,6 +215,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // a copy of CTA 1 that CTA 0 no longer counted has no barrier to wait on:
+    // 0.1 ms for it to land
+    if (*gave_up && threadIdx.x == 0)
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
     __syncwarp();
     cluster_sync();   // no CTA leaves while the other may still signal it
     if (warp == 1) {

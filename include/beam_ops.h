@@ -194,6 +194,15 @@ int beam_route_scores(void *stream, const float *logits, int T, int E, long long
  */
 int beam_ops_status(void *stream);
 
+/*
+ * For tests of the bounded waits: the calling thread's next beam_mx_matmul that
+ * launches waits in stage `stage` of K (256 4-bit or 128 8-bit elements a stage;
+ * -1: none) for bytes that do not come, limit_ms (1 .. 2000) at a wait.  Where it
+ * has that stage it ends within some 20 such limits, its result is not valid
+ * and beam_ops_status reports BEAM_ERR_TIMEOUT.
+ */
+int beam_ops_debug_withhold(int stage, int limit_ms);
+
 /* Text of the last host-side error of a call above on the calling thread. */
 const char *beam_ops_error(void);
 

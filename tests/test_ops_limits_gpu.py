@@ -6,7 +6,7 @@ import torch
 
 import ops_ref as R
 from group_limited_routing_sigmoid_b200 import ops
-from group_limited_routing_sigmoid_b200.binding import BEAM_ERR_INVALID_ARG
+from group_limited_routing_sigmoid_b200.binding import BEAM_ERR_INVALID_ARG, BEAM_ERR_TIMEOUT, library
 from group_limited_routing_sigmoid_b200.build import build
 
 pytestmark = pytest.mark.gpu
@@ -135,3 +135,45 @@ def test_status_is_refused_in_a_capture_that_goes_on():
     g.replay()
     assert ops.ops_status() == 0
     assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp8"])
+@pytest.mark.parametrize("T,N,K,stages", [(1, 256, 2048, (0, 5)), (20, 300, 1024, (0, 3)), (64, 200, 256, (0,)),
+                                          (300, 300, 512, (0, 1)), (64, 40000, 512, (0, 1)), (1000, 3333, 512, (1,)),
+                                          (2100, 1200, 512, (0, 1))])
+def test_waits_that_run_out_end_and_are_reported_once(fmt, T, N, K, stages):
+    """Bytes that do not come, in a product's first stage (nothing issued yet) and in a later one (copies and MMAs in flight):
+    split tiles, whole ones, persistent ones and pairs.  The next product is skipped, the one after the report is right."""
+    g = torch.Generator().manual_seed(T + N)
+    a, w = (ops.mx_quantize(torch.randn(n, K, generator=g).bfloat16().cuda(), fmt, "tiled") for n in (T, N))
+    want = ops.mx_matmul(a, w)
+    assert ops.ops_status() == 0
+    for stage in stages:
+        assert library().beam_ops_debug_withhold(stage, 5) == 0
+        ops.mx_matmul(a, w)
+        skipped = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        ops.mx_matmul(a, w, out=skipped)
+        assert ops.ops_status() == BEAM_ERR_TIMEOUT
+        assert ops.ops_status() == 0
+        assert (skipped == 7.0).all()
+        assert torch.equal(ops.mx_matmul(a, w), want)
+        assert ops.ops_status() == 0
+
+
+def test_one_of_two_callers_gets_an_event():
+    import threading
+
+    a = ops.mx_quantize(torch.randn(64, 512, generator=torch.Generator().manual_seed(1)).cuda(), "mxfp8", "tiled")
+    want = ops.mx_matmul(a, a)
+    for _ in range(10):
+        library().beam_ops_debug_withhold(0, 1)
+        ops.mx_matmul(a, a)
+        torch.cuda.synchronize()
+        got, streams = [], [torch.cuda.Stream() for _ in range(4)]
+        threads = [threading.Thread(target=lambda s=s: got.append(ops.ops_status(stream=s))) for s in streams]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert sorted(got) == [BEAM_ERR_TIMEOUT, 0, 0, 0]
+    assert torch.equal(ops.mx_matmul(a, a), want)

@@ -26,3 +26,9 @@ def test_quantize_nvfp4_refuses(lib, kw):
     x, g, codes, scales = (a[n] and P(a[n]) for n in ("x", "g", "codes", "scales"))
     assert lib.beam_mx_quantize_nvfp4(None, x, a["dtype"], a["rows"], a["K"], a["ldx"], a["layout"], g, codes, scales) == INVALID
     assert lib.beam_ops_error()
+
+
+def test_withhold_refuses(lib):
+    for stage, ms in ((-2, 10), (0, 0), (0, -1), (0, 2001)):
+        assert lib.beam_ops_debug_withhold(stage, ms) == INVALID
+    assert lib.beam_ops_debug_withhold(-1, 1) == binding.BEAM_OK
