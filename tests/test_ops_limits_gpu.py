@@ -177,3 +177,23 @@ def test_one_of_two_callers_gets_an_event():
             t.join()
         assert sorted(got) == [BEAM_ERR_TIMEOUT, 0, 0, 0]
     assert torch.equal(ops.mx_matmul(a, a), want)
+
+
+@pytest.mark.parametrize("E", [2, 3, 8, 60, 256, 1000])
+@pytest.mark.parametrize("spread", [1.0, 4.0, 12.0, 30.0])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_softmax_weights_far_below_the_largest(E, spread, renorm):
+    """Scores of every size: the rounding of logit - maximum does not reach the weights.  In half ulps: the exponential 4, its
+    correction 1, what the sum's terms hold 4 + 10 and its additions ceil(E / 32) + 4, the division and the scale 2."""
+    g = torch.Generator().manual_seed(E)
+    l = (torch.randn(3000, E, generator=g) * spread).cuda()
+    k = min(4, E)
+    for bias in (None, (torch.rand(E, generator=g) * 1e-3).cuda()):
+        idx, w = ops.route_scores(l, k, score="softmax", bias=bias, renormalize=renorm)
+        x = l.double()
+        p = torch.exp(x - x.amax(1, keepdim=True))
+        p = (p / p.sum(1, keepdim=True)).gather(1, idx.long())
+        if renorm:
+            p = p / p.sum(1, keepdim=True)
+        tol = (4 + 1 + 14 + (E + 31) // 32 + 4 + 2) * 2.0 ** -24 * p + 2.0 ** -149
+        assert ((w.double() - p).abs() <= tol).all(), float(((w.double() - p).abs() / tol).max())
