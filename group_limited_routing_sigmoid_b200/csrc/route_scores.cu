@@ -220,8 +220,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
     const Span my = span_of(p, lane);
     float *cand = s_key[warp];
     int *expert = s_expert[warp];
-    // with a bias one more than top_k: the best that is not chosen
-    const int want = BIAS ? p.top_k + 1 : p.top_k;
+    // with a bias one more than top_k: the best that is not chosen (33 have no
+    // lane each: top_k 32 looks for that one by itself, 4096 x 256: 17 us, 43
+    // with every such row decided in 64 bits)
+    const int want = BIAS && p.top_k < 32 ? p.top_k + 1 : p.top_k;
     float bias[BIAS ? EPL : 1];
     bool nan_bias = false;
     if constexpr (BIAS) {
@@ -428,9 +430,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL <= 8 ? 4 : 2) route_scor
             __syncwarp();
             const bool check = lane < p.top_k && in;
             const float k0 = check ? cand[lane] : 0.f;
-            const float k1 = check && lane + 1 < n ? cand[lane + 1] : bound;
+            float border = bound;   // no key that is no candidate is above it
+            if (want == p.top_k) {
+                border = -3.402823466e38f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) border = fmaxf(border, key[i] < bound ? key[i] : border);
+                border = redux_max(border);
+            }
+            const float k1 = check && lane + 1 < n ? cand[lane + 1] : border;
             const float tol = tol_score + 0x1p-22f * (fabsf(k0) + fabsf(k1));
-            const bool outside = check && lane == p.top_k - 1 && !(k0 - bound > tol);
+            const bool outside = check && lane == p.top_k - 1 && !(k0 - border > tol);
             const bool near = check && lane + 1 < n && !(k0 - k1 > tol) &&
                               !(lane + 1 < p.top_k && tie[lane].x == tie[lane + 1].x && tie[lane].y == tie[lane + 1].y);
             if (__any_sync(0xffffffffu, outside)) {

@@ -197,3 +197,20 @@ def test_softmax_weights_far_below_the_largest(E, spread, renorm):
             p = p / p.sum(1, keepdim=True)
         tol = (4 + 1 + 14 + (E + 31) // 32 + 4 + 2) * 2.0 ** -24 * p + 2.0 ** -149
         assert ((w.double() - p).abs() <= tol).all(), float(((w.double() - p).abs() / tol).max())
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,keep", [(32, 1, 1), (33, 1, 1), (40, 1, 1), (64, 1, 1), (256, 1, 1), (256, 8, 4), (1000, 1, 1), (720, 10, 4)])
+def test_route_of_the_largest_top_k_with_a_bias(score, E, G, keep):
+    """32 chosen leave no lane for the best that is not: ties and near ties across that border, masks that leave 31 to 33."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(64, E, generator=g)
+    order = l[8:24].argsort(dim=1, descending=True)
+    for i, n in enumerate((31, 32, 33, 34) * 4):       # the n best alone are not masked
+        l[8 + i].scatter_(0, order[i, n:], -float("inf"))
+    l[24:32] = l[24:32].to(torch.bfloat16).float()
+    l[32:40] = torch.round(l[32:40])
+    l[40:48] = 0.5 + torch.arange(E) * 2.0 ** -24      # neighbours one ulp apart
+    l = l.cuda()
+    for bias in (torch.zeros(E), torch.randn(E, generator=g) * 0.05, torch.randn(E, generator=g) * 1e-8):
+        check_route(l, 32, score, bias.cuda(), G, keep)
