@@ -214,3 +214,62 @@ def test_route_of_the_largest_top_k_with_a_bias(score, E, G, keep):
     l = l.cuda()
     for bias in (torch.zeros(E), torch.randn(E, generator=g) * 0.05, torch.randn(E, generator=g) * 1e-8):
         check_route(l, 32, score, bias.cuda(), G, keep)
+
+
+@pytest.mark.parametrize("af,wf", [("nvfp4", "nvfp4"), ("mxfp4", "mxfp4"), ("mxfp8", "mxfp4"), ("mxfp8", "mxfp8")])
+@pytest.mark.parametrize("T,N,K", [(6, 70, 256), (70, 6, 256), (300, 300, 512), (2100, 1200, 256)])
+def test_values_that_are_not_finite_reach_their_row_and_column_alone(af, wf, T, N, K):
+    """What the quantiser writes for a block with an infinity or a NaN, codes of zero under a scale of NaN, makes the whole row
+    (of a) or column (of w) of the product NaN, and nothing else; so does a tensor scale out of range."""
+    g = torch.Generator().manual_seed(T)
+    x, w = torch.randn(T, K, generator=g).cuda(), torch.randn(N, K, generator=g).cuda()
+    x[2, 5], w[3, K - 1] = float("nan"), float("inf")
+    a, b = ops.mx_quantize(x, af, "tiled"), ops.mx_quantize(w, wf, "tiled")
+    bad = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    bad[2], bad[:, 3] = True, True
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(ops.mx_matmul(a, b, dtype).isnan(), bad)
+    if af == "nvfp4":
+        far = ops.mx_quantize(x, af, "tiled", torch.full((1,), 2.0 ** 113, device="cuda"))
+        assert ops.mx_matmul(far, b).isnan().all()
+    assert ops.ops_status() == 0
+
+
+def test_norm_repeats_itself_and_its_codes_differ_next_to_ties_alone():
+    """The same bits every time; and where a code or a scale is not that of the exact row, the exact value lies within the FP32
+    row's own error of the border between the two."""
+    T, H = 2048, 5120
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(T, H, generator=g, device="cuda") * 3).bfloat16()
+    r = torch.randn(T, H, generator=g, device="cuda")
+    gamma = 1 + 0.02 * torch.randn(H, generator=g, device="cuda")
+    alpha, beta = float(np.float32(np.sqrt(19 / 20))), float(np.float32(np.sqrt(1 / 20)))
+    runs = [ops.rms_norm(x, gamma, residual=r, alpha=alpha, beta=beta, quantize="mxfp8", layout="rows") for _ in range(4)]
+    for o in runs[1:]:
+        assert torch.equal(o.out, runs[0].out) and torch.equal(o.residual, runs[0].residual)
+        assert torch.equal(o.quantized.codes, runs[0].quantized.codes) and torch.equal(o.quantized.scales, runs[0].quantized.scales)
+    q = runs[0].quantized
+    s = beta * x.double() + alpha * r.double()
+    scale = 1 / torch.sqrt((s * s).mean(1, keepdim=True) + float(np.float32(1e-6)))
+    y = s * scale * gamma.double()
+    # s: two products and a sum; the mean of squares: at most 16 fused terms and 10 joins a thread, twice what s is off, and half
+    # of both reaches y; root, division and two products
+    u = 2.0 ** -24
+    ds = 2 * u * ((beta * x.double()).abs() + (alpha * r.double()).abs())
+    ds_row = (ds * ds).mean(1, keepdim=True).sqrt() * scale
+    dy = y.abs() * ((0.5 * (16 + 10 + 2) + 5) * u + ds_row) + ds * scale * gamma.double()
+    amax, damax = y.abs().view(T, -1, 32).amax(-1), dy.view(T, -1, 32).amax(-1)
+
+    def exponent(a):                                   # least k with a <= 448 x 2^k
+        m, e = torch.frexp(a)
+        return torch.where(m <= 0.875, e - 9, e - 8)
+    k = q.scales.int() - 127
+    assert ((k == exponent(amax)) | (exponent(amax - damax) != exponent(amax + damax))).all()
+    p = torch.exp2(k.double()).repeat_interleave(32, dim=1)
+    grid = torch.from_numpy(R.E4M3).cuda()
+    code = (q.codes & 127).long()
+    mid = (grid[1:] + grid[:-1]) / 2
+    border = torch.cat([torch.tensor([0.0], dtype=torch.float64, device="cuda"), mid, torch.tensor([1e9], dtype=torch.float64, device="cuda")])
+    assert (y.abs() + dy >= border[code] * p).all() and (y.abs() - dy <= border[code + 1] * p).all()
+    off = (y.abs() < border[code] * p) | (y.abs() > border[code + 1] * p)
+    assert off.double().mean() < 1e-4
