@@ -232,6 +232,7 @@ __device__ __forceinline__ void flush_row(const uint8_t *line, int row, int u, u
 __device__ __forceinline__ void flush_lines(const uint8_t *stg, int lane, int dtype, void *out, size_t at, long long ldo,
                                             int rows, int cols, bool vec)
 {
+    if (rows <= 0 || cols <= 0) return;   // the tile reaches past out; no lane has lines to share
     const int es = dtype == BEAM_F32 ? 4 : 2, per = 16 / es;
     __syncwarp();
     uint8_t *o = static_cast<uint8_t *>(out) + at * es;
