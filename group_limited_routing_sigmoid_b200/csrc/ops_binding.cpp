@@ -478,17 +478,18 @@ PyObject *route_scores(PyObject *const *a, Py_ssize_t n)
     const Rows r(l, "logits");
     if (r.code != BEAM_F32) raise_type("%s: expected torch.float32, got %s", "logits", shape_of(l));
     const int T = r.height("logits"), E = r.columns("logits"), top_k = small_integer(a[1]);
-    const long long k = top_k > 0 ? top_k : 0;   // refused below
+    const bool refused = top_k < 1 || top_k > 32;   // by the library, before any output is made
+    const long long k = refused ? 0 : top_k;
     const On on(l);
     const float *bias = flat_or_null<float>(a[3], "bias", at::kFloat, E, &l);
     at::Tensor idx, w;
-    if (a[9] == Py_None) {
+    if (refused || a[9] == Py_None) {
         idx = fresh({T, k}, at::kInt, l);
     } else {
         flat<int32_t>(a[9], "idx", at::kInt, T * k, &l);
         idx = THPVariable_Unpack(a[9]);
     }
-    if (a[10] == Py_None) {
+    if (refused || a[10] == Py_None) {
         w = fresh({T, k}, at::kFloat, l);
     } else {
         flat<float>(a[10], "w", at::kFloat, T * k, &l);

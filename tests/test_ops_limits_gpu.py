@@ -273,3 +273,15 @@ def test_norm_repeats_itself_and_its_codes_differ_next_to_ties_alone():
     assert (y.abs() + dy >= border[code] * p).all() and (y.abs() - dy <= border[code + 1] * p).all()
     off = (y.abs() < border[code] * p) | (y.abs() > border[code + 1] * p)
     assert off.double().mean() < 1e-4
+
+
+def test_route_refuses_a_top_k_before_it_makes_outputs():
+    l = torch.randn(60000, 64, device="cuda")
+    some = torch.empty(60000, 33, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocated_bytes.all.allocated"]
+    for k in (2 ** 31 - 1, 33, 0, -1):
+        for idx in (None, some):
+            with pytest.raises(ops.BeamMoEError, match="top_k"):
+                ops.route_scores(l, k, idx=idx)
+    assert torch.cuda.memory_stats()["allocated_bytes.all.allocated"] == before
