@@ -14,6 +14,10 @@ kernels of a few microseconds.  Every call runs on the device of its tensors,
 on ``stream`` or that device's current stream.  Where ``stream`` is another
 one than the current stream, the caller orders the two for the inputs; outputs
 are made on ``stream`` and both are marked as used there.
+
+For inference: there is no backward pass.  Inputs may require a gradient (a
+layer's parameters do), results never do and nothing is recorded, also where
+gradients are enabled.
 """
 from __future__ import annotations
 
@@ -253,7 +257,9 @@ def route_scores(logits: torch.Tensor, top_k: int, score: str = "sigmoid", bias:
     Scores are sigmoid(logit) or the row's softmax; `bias` (fp32 [E]) steers
     the choice only; with topk_group < n_group the groups are ranked by the
     sum of their `group_top` best keys first.  A logit of -inf masks an
-    expert; slots with no expert left get index -1, weight 0."""
+    expert; slots with no expert left get index -1, weight 0.  Near ties are
+    decided in 64 bits, by the handle's router (BeamMoE.route_logits) in FP32:
+    use that one beside a handle's own routing."""
     s = _key(SCORES, score, "score")
     f = (_binding or _native()).route_scores
     if stream is None:

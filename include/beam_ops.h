@@ -168,9 +168,16 @@ typedef enum { BEAM_SCORE_SIGMOID = 0, BEAM_SCORE_SOFTMAX = 1 } beam_score;
  *        group_top (1 or 2) largest keys, the topk_group best groups stay;
  *   the top_k largest keys are chosen, in descending order;
  *   w    p of the chosen, divided by their sum if renormalize, times scale.
- * Ties go to the lower index.  The choices are those of exact arithmetic on
+ * Ties go to the lower index.  The choices are those of 64-bit arithmetic on
  * the FP32 logits and biases: where FP32 keys are too close to tell, the row
- * is decided in 64 bits.
+ * is decided in 64 bits, and keys or group scores that are equal there (sums
+ * with sigmoids that saturate at 1, groups whose softmax is below 2^-1074) tie.
+ * Without a bias experts are ordered by their logits, which are exact.
+ * The handle's router (beam_moe_route, beam_moe_route_logits) decides such near
+ * ties in FP32, so the two may choose differently there (below 1% of rows of
+ * random logits).  Use the handle's with a handle's block, so that routing and
+ * block agree with what the block does by itself, and this one for logits of
+ * other routers, softmax, masks and other group rules.
  * An expert whose logit is -inf is masked: it has p = 0, is never chosen, and
  * counts for no group; a bias of -inf does the latter two.  Slots that no
  * expert is left for get index -1 and weight 0.  A row that holds a NaN, or +inf under softmax, or

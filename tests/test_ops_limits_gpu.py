@@ -285,3 +285,15 @@ def test_route_refuses_a_top_k_before_it_makes_outputs():
             with pytest.raises(ops.BeamMoEError, match="top_k"):
                 ops.route_scores(l, k, idx=idx)
     assert torch.cuda.memory_stats()["allocated_bytes.all.allocated"] == before
+
+
+def test_inputs_that_require_a_gradient_give_results_that_do_not():
+    x = torch.randn(8, 256, device="cuda", requires_grad=True)
+    gamma = torch.nn.Parameter(torch.ones(256, device="cuda"))
+    n = ops.rms_norm(x, gamma, residual=x, quantize="mxfp8")
+    q = ops.mx_quantize(x, "mxfp8", "tiled")
+    results = [n.out, n.residual, ops.mx_matmul(n.quantized, q), ops.mx_dequantize(q), *ops.route_scores(x, 4), ops.mx_tensor_scale(x)]
+    assert not any(t.requires_grad for t in results)
+    with torch.no_grad():
+        again = ops.rms_norm(x, gamma, residual=x)
+    assert torch.equal(again.out, n.out)
