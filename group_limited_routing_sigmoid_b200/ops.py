@@ -156,6 +156,8 @@ def _operand(q, name: str):
 def _given(q, name: str, format: str, layout: str, x):
     """Codes and scales of an operand to write into: of this format and layout and x's shape."""
     codes, scales, _, _, _, rows, K = _operand(q, name)
+    if codes is None or scales is None:
+        raise TypeError(f"{name}: an operand to write into has codes and scales")
     if (q.format, q.layout, rows, K) != (format, layout, *x.shape):
         raise ValueError(f"{name}: {q.format} {q.layout} {rows} x {K}, not {format} {layout} {tuple(x.shape)}")
     return codes, scales

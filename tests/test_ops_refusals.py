@@ -2,8 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from group_limited_routing_sigmoid_b200 import binding
+from group_limited_routing_sigmoid_b200 import binding, ops
 from group_limited_routing_sigmoid_b200.build import build
 
 INVALID = binding.BEAM_ERR_INVALID_ARG
@@ -32,3 +33,10 @@ def test_withhold_refuses(lib):
     for stage, ms in ((-2, 10), (0, 0), (0, -1), (0, 2001)):
         assert lib.beam_ops_debug_withhold(stage, ms) == INVALID
     assert lib.beam_ops_debug_withhold(-1, 1) == binding.BEAM_OK
+
+
+def test_an_operand_to_write_into_has_codes_and_scales():
+    x, some = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.uint8)
+    for codes, scales in ((None, some), (some, None)):
+        with pytest.raises(TypeError, match="codes and scales"):
+            ops.mx_quantize(x, "mxfp4", out=ops.MxTensor(codes, scales, "mxfp4", "rows", 4, 64))
