@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok) {
+            {
+                // copies in flight land before the CTA exits, also where their readers gave up (time-bounded)
                 const long long n = issued < C::STAGES ? issued : C::STAGES;
                 int s = stage;
                 uint32_t ph = phase;

@@ -197,9 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (!ok && lane == 0) {
-            // Give the copies already in flight time to land before the CTA
-            // exits: wait (time-bounded, status ignored) on the last ones.
+        if (lane == 0) {
+            // The copies in flight land before the CTA exits, also where the
+            // readers gave up after the last was issued: wait (time-bounded,
+            // status ignored) on the last ones.
             long long n = issued < C::STAGES ? issued : C::STAGES;
             int s = stage;
             uint32_t ph = phase;

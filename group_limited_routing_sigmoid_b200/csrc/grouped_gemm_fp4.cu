@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                     ring_step(rs, rp, C::RAW_STAGES);
                 }
             }
-            if (!ok) {
-                // copies in flight land before the CTA leaves (time-bounded)
+            {
+                // copies in flight land before the CTA leaves, also where their readers gave up (time-bounded)
                 const long long m = issued < C::RAW_STAGES ? issued : C::RAW_STAGES;
                 int s = rs;
                 uint32_t ph = rp;

@@ -79,7 +79,7 @@ __device__ __forceinline__ void ring_next(int &s, uint32_t &ph, int n)
 
 // Wait (time-bounded, status ignored) for the last min(issued, n) copies a
 // ring's producer issued to land, so that no copy is in flight when the CTA
-// leaves after a failed wait.  CTA 0's barriers count both CTAs' copies.
+// leaves, also where its readers gave up.  CTA 0's barriers count both CTAs' copies.
 __device__ __forceinline__ void drain_ring(uint64_t *full, int s, uint32_t ph, long long issued,
                                            int n, long long limit_ns)
 {
@@ -208,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     ring_next(sa, pa, SA);
                 }
             }
-            if (!ok && rank == 0) drain_ring(fullA, sa, pa, issued, SA, p.ctl.limit_ns);
+            if (rank == 0) drain_ring(fullA, sa, pa, issued, SA, p.ctl.limit_ns);
         }
     } else if (warp == kPairThreads / 32 - 1) {
         // ------------------------------------------------ token-row producer
@@ -265,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ring_next(sb, pb, SB);
             }
         }
-        if (!ok && lane == 0 && rank == 0) drain_ring(fullB, sb, pb, issued, SB, p.ctl.limit_ns);
+        if (lane == 0 && rank == 0) drain_ring(fullB, sb, pb, issued, SB, p.ctl.limit_ns);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ------------------------------------------------ UMMA issuer (CTA 0)
         int sa = 0, sb = 0;

@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(192, 1)
                 }
             }
         }
-        if (!ok) {
+        {
+            // copies in flight land before the CTA exits, also where their readers gave up (time-bounded)
             long long n = issued < kRStages ? issued : kRStages;
             int st = stage;
             uint32_t ph = phase;
