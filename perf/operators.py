@@ -368,7 +368,8 @@ def _run_own(c):
     from group_limited_routing_sigmoid_b200 import ops
 
     if c["op"] == "norm":
-        r = ops.rms_norm(c["xv"], c["gamma"], residual=c.get("rv"), alpha=c["alpha"], beta=c["beta"],
+        # without a residual the rows are normalised as they are, unscaled
+        r = ops.rms_norm(c["xv"], c["gamma"], residual=c.get("rv"), alpha=c["alpha"], beta=c["beta"] if "rv" in c else 1.0,
                          eps=1e-6, dtype=DT[c["out"]], quantize="mxfp8" if c["q"] else None, layout=c["layout"])
         out = {"out": r.out}
         if r.residual is not None:
