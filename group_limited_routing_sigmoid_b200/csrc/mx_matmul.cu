@@ -25,11 +25,11 @@
 //   one sequence, NVFP4 5120 x 20480 (59 MB): 13.5 us = 4.4 TB/s.  About 3 us
 //     are launch, set-up and the sum over a cluster; the stream itself runs at
 //     5.5 TB/s (37888 x 20480: 79 us), the scales' copies taking 8% of it.
-//   64 tokens, MXFP8 x MXFP4, 20480 x 5120 (56 MB): 21.8 us = 2.7 TB/s.  Copies
-//     that spread 4-bit codes cost the TMA unit 3 clocks a row of 64 bytes of
-//     codes, as much as for 128 bytes of others, and the token rows as many
-//     again by half; and 160 tiles leave 12 of 148 SMs with two.  Weights on
-//     the B side in tiles of 192, tokens on A, took 25.6 us.
+//   64 tokens, MXFP8 x MXFP4, 20480 x 5120 (56 MB): 22.4 us = 2.6 TB/s.  The TMA
+//     unit takes about 3 clocks a row of a box, 64 bytes of 4-bit codes (spread
+//     or not, the time is the same) as long as 128 bytes of others, and the
+//     token rows cost as many again by half; and 160 tiles leave 12 of 148 SMs
+//     with two.  Weights on the B side in tiles of 192, tokens on A, took 25.6 us.
 //   L2 prefetches of the codes 6 or 12 stages ahead made all of them slower
 //     (79 -> 95 us, 27 -> 32 us).
 #include <atomic>

@@ -8,6 +8,13 @@
 // memory, one buffer (the scales of the ring's stages take the rest): the
 // epilogue empties it into registers first (128 a thread), hands it back, and
 // rounds and stores while the next tile's MMAs run.
+//
+// 4096 x 10240 x 5120, and the same kernel with parts left out (us): NVFP4 110,
+// 85 without the scale copies, 98 without the MMAs, 70 with the loads alone;
+// MXFP4 88, 84, 75, 69; MXFP8 x MXFP4 155, 140, 111, 108.  So the loads (64 KB
+// a pair and stage) are the largest part of the 4-bit kinds' time; NVFP4's 12
+// copies a stage share the tensor pipe with the MMAs and add 26 us, MXFP4's
+// 6 add 4, MXFP8's 3 (in twice the stages) 15.
 #include "mx_matmul.cuh"
 
 namespace beam {

@@ -14,8 +14,11 @@
 //
 // 20480 x 5120 bf16 on a B200: tensor scale 35 us (6.0 TB/s), NVFP4 46 us
 // (5.8 TB/s; tiled scales 55 us), MXFP8 tiled 53 us (6.0 TB/s), NVFP4 back to
-// bf16 45 to 48 us (5.6 to 6.0 TB/s).  With 8 elements a lane, one load ahead
-// and scalar arithmetic the first two and the last took 195 us together, now 133.
+// bf16 45 to 48 us (5.6 to 6.0 TB/s).  Tiled scales of short rows cost more: at
+// 64 elements an MX row's two scales are padded to four, so half of the chunks
+// are padding (400000 x 64 MXFP4: 27 us tiled, 10.5 in rows).  With 8 elements a
+// lane, one load ahead and scalar arithmetic tensor scale, NVFP4 and read-back
+// took 195 us together, now 133.
 #include "ops_common.cuh"
 
 namespace beam {
@@ -483,7 +486,9 @@ __global__ void __launch_bounds__(kThreadsQ) mx_dequantize_kernel(const DequantA
     }
 }
 
-// Scales from rows to tiles: a thread per 4-byte group of a tile row.
+// Scales from rows to tiles: a thread per 4-byte group of a tile row.  Run once
+// for a checkpoint: 20480 x 5120 NVFP4 12.5 us for 13.1 MB in and out, MXFP4 7.6
+// us for 6.6 MB (1 TB/s: single-byte loads, 4-byte stores 16 bytes apart).
 __global__ void mx_tile_scales_kernel(const uint8_t *scales, uint8_t *tiled, long long rows, ScaleMap map,
                                       long long groups)
 {

@@ -6,11 +6,11 @@
 // experts whose key reaches the n-th largest of the lanes' best keys (n the
 // experts wanted) hold the n largest and are few (about 13 of 256 for n = 9).
 // They are packed, one to a lane, and ranked by counting the larger ones.
-// 32768 x 256, 8 groups of which 4 stay, bias, top 8: 33 us (1.07 TB/s); without
-// groups and bias 21 us.  Lists sorted in the lanes with one maximum over their
+// 32768 x 256, 8 groups of which 4 stay, bias, top 8: 33 to 35 us (1.0 TB/s); without
+// groups and bias 20 us.  Lists sorted in the lanes with one maximum over their
 // heads per expert wanted took 49 and 26 us.
 //
-// Decisions are those of exact arithmetic: an FP32 score is off by a few
+// Decisions are those of 64-bit arithmetic: an FP32 score is off by a few
 // ulps, so a row in which two keys (neighbours of the chosen ranking) or two
 // group scores (last kept, first dropped) are closer than that error, and not
 // exactly equal, is decided again from 64-bit scores (decide_row, the same

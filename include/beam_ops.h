@@ -31,7 +31,7 @@ typedef enum { BEAM_BF16 = 0, BEAM_F16 = 1, BEAM_F32 = 2 } beam_dtype;
 
 /*
  * Microscaled formats: blocks of consecutive elements of a row share a scale.
- *   NVFP4  E2M1 elements, an E4M3 scale per 16, an FP32 scale per tensor;
+ *   NVFP4  E2M1 elements, an E4M3 scale per 16 (sign bit 0), an FP32 scale per tensor;
  *   MXFP4  E2M1 elements, a power of two (UE8M0 byte: 2^(byte - 127)) per 32;
  *   MXFP8  E4M3 elements, a power of two per 32.
  * Codes: two E2M1 a byte, element 2j of a row in the low nibble of byte j
