@@ -104,7 +104,12 @@ __device__ __forceinline__ float exp_of_difference(float x, float y)
     return e > 0.f ? fmaf(e, lost, e) : 0.f;   // d = -inf has no such factor
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// From e^-|x|, which does not overflow: scores down to the least subnormal.
+__device__ __forceinline__ float sigmoid(float x)
+{
+    const float e = expf(-fabsf(x));
+    return (x < 0.f ? e : 1.0f) / (1.0f + e);
+}
 
 // --- a row in 64 bits ------------------------------------------------------------
 

@@ -297,3 +297,17 @@ def test_inputs_that_require_a_gradient_give_results_that_do_not():
     with torch.no_grad():
         again = ops.rms_norm(x, gamma, residual=x)
     assert torch.equal(again.out, n.out)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_weights_down_to_the_least_subnormal(renorm):
+    """exp(-x) overflows below -88.7, the score only vanishes below -104.  In half ulps: the exponential 4, sum, division, scale
+    and, renormalised, up to 5 joins and another division; half the least subnormal each where the result is one."""
+    l = torch.cat([torch.linspace(-106, -80, 500), torch.linspace(-1, 40, 140)]).view(-1, 1).repeat(1, 4)
+    l += torch.arange(4) * -0.37
+    idx, w = ops.route_scores(l.cuda(), 4, renormalize=renorm)
+    assert (idx == torch.arange(4, device="cuda")).all()
+    p = 1 / (1 + torch.exp(-l.double()))
+    if renorm:
+        p = p / p.sum(1, keepdim=True)
+    assert ((w.cpu().double() - p).abs() <= 14 * 2.0 ** -24 * p + 4 * 2.0 ** -149).all()
