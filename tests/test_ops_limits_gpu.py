@@ -311,3 +311,37 @@ def test_sigmoid_weights_down_to_the_least_subnormal(renorm):
     if renorm:
         p = p / p.sum(1, keepdim=True)
     assert ((w.cpu().double() - p).abs() <= 14 * 2.0 ** -24 * p + 4 * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("name", ["decode_small", "decode_small_nvfp4", "dense_tiny"])
+def test_beside_a_handles_block_on_another_stream(name):
+    """A block's forward and the operators at once, each on its own stream: both use tensor memory, and give what they give alone."""
+    from group_limited_routing_sigmoid_b200 import workloads as W
+    from group_limited_routing_sigmoid_b200.binding import BeamMoE
+
+    wl = W.WORKLOADS[name]
+    d = W.make_inputs(wl, "cuda")
+    if name.endswith("nvfp4"):
+        E, I, H = wl.n_experts, wl.inter, wl.hidden
+        for n, rows, K in (("gate", I, H), ("up", I, H), ("down", H, I)):
+            q = ops.mx_quantize(torch.randn(E * rows, K, device="cuda").mul_(0.02).bfloat16(), "nvfp4")
+            d[n + "_codes"], d[n + "_scales"] = q.codes.view(E, rows, K // 2), q.scales.view(E, rows, K // 16)
+            d[n + "_global"] = float(q.tensor_scale)
+    moe = BeamMoE.from_workload(wl, d)
+    out = torch.empty_like(d["x"])
+    moe.forward(d["x"], out=out)
+    want = out.clone()
+    g = torch.Generator().manual_seed(2)
+    pairs = [tuple(ops.mx_quantize(torch.randn(n, K, generator=g).bfloat16().cuda(), fmt, "tiled") for n in (T, N))
+             for fmt, T, N, K in (("nvfp4", 1, 5120, 5120), ("mxfp8", 64, 20480, 640), ("mxfp4", 500, 500, 512), ("nvfp4", 2048, 2048, 512))]
+    alone = [ops.mx_matmul(a, w) for a, w in pairs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        moe.forward(d["x"], out=out)
+        with torch.cuda.stream(side):
+            got = [ops.mx_matmul(a, w) for a, w in pairs]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and moe.get_status() == 0 and ops.ops_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, alone))
+    moe.close()
