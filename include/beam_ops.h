@@ -135,7 +135,9 @@ int beam_mx_matmul(void *stream, int a_format, const uint8_t *a_codes, const uin
  * Residual addition and root-mean-square norm of T rows of H elements:
  *     s = alpha * residual + beta * x       (s = beta * x without residual)
  *     y = s / sqrt(mean(s^2) + eps) * gamma
- * in FP32; residual_out = s and out = y, each rounded once.  With
+ * in FP32 (where the sum of s^2 overflows, at elements of 1.8e19 and more, the
+ * finite elements of the row give y = 0); residual_out = s and out = y, each
+ * rounded once.  With
  * alpha = sqrt((k-1)/k), beta = 1/sqrt(k) this is the depth-scaled residual
  * update that beam_moe_forward applies after a block, in front of the next.
  * x            [T, H] x_dtype, rows ldx apart.
